@@ -1,0 +1,185 @@
+// dropout.cu -- dropout whose mask is drawn again wherever it is needed
+// (include/mqc.h: mqc_dropout_fwd, mqc_dropout_bwd).
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "dense.cuh"
+#include "host.h"
+
+namespace mqc {
+namespace {
+
+// Philox4x32-10 (Salmon et al., "Parallel random numbers: as easy as 1, 2,
+// 3", SC 2011): ten rounds of two 32 x 32 -> 64-bit products.  The 64-bit
+// variant that the stochastic quantizer uses would cost about twice the
+// instructions per random bit here, and this pass is close to issue-bound.
+__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1) {
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t p = static_cast<uint64_t>(c.x) * 0xD2511F53u, q = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
+        c = make_uint4(static_cast<uint32_t>(q >> 32) ^ c.y ^ k0, static_cast<uint32_t>(q),
+                       static_cast<uint32_t>(p >> 32) ^ c.w ^ k1, static_cast<uint32_t>(p));
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return c;
+}
+
+struct DropoutParams {
+    const void *x, *res;
+    void *y;
+    int64_t ldx, ldr, ldy, cols, total;   // total = rows * cols
+    uint64_t seed, offset;
+    const uint64_t *offset_dev;
+    uint32_t drop;                        // an element stays when its 16 bits are >= drop
+    float scale;
+};
+
+// A thread owns one Philox block: eight consecutive elements of the logical
+// row-major matrix.  VEC: the eight are contiguous in every tensor and start
+// at 16-byte boundaries (one long row, or rows of whole blocks); a last,
+// partial block and everything else goes element by element.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams P) {
+    const uint64_t offset = P.offset + (P.offset_dev ? *P.offset_dev : 0);
+    const uint32_t k0 = static_cast<uint32_t>(P.seed), k1 = static_cast<uint32_t>(P.seed >> 32);
+    const int64_t blocks = (P.total + 7) / 8;
+    const T *x = static_cast<const T *>(P.x), *res = static_cast<const T *>(P.res);
+    T *y = static_cast<T *>(P.y);
+    constexpr int n = Vec<T>::n;
+    for (int64_t b = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; b < blocks;
+         b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t i0 = b * 8;
+        int64_t row = 0, col = i0;
+        if (P.cols != P.total) {
+            row = P.total <= 0xFFFFFFFFll ? static_cast<uint32_t>(i0) / static_cast<uint32_t>(P.cols) : i0 / P.cols;
+            col = i0 - row * P.cols;
+        }
+        if (VEC && i0 + 8 <= P.total) {
+            uint4 xv[8 / n], rv[8 / n];
+#pragma unroll
+            for (int v = 0; v < 8 / n; ++v) xv[v] = reinterpret_cast<const uint4 *>(x + row * P.ldx + col)[v];
+            if (res)
+#pragma unroll
+                for (int v = 0; v < 8 / n; ++v) rv[v] = reinterpret_cast<const uint4 *>(res + row * P.ldr + col)[v];
+            const uint4 r = philox4x32_10(make_uint4(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32),
+                                                     static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)),
+                                          k0, k1);
+            const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+            for (int v = 0; v < 8 / n; ++v) {
+                float f[n];
+                Vec<T>::widen(xv[v], f);
+#pragma unroll
+                for (int q = 0; q < n; ++q) {
+                    const int e = v * n + q;
+                    const uint32_t bits = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu;
+                    f[q] = bits >= P.drop ? f[q] * P.scale : 0.f;
+                }
+                if (res) {
+                    float a[n];
+                    Vec<T>::widen(rv[v], a);
+#pragma unroll
+                    for (int q = 0; q < n; ++q) f[q] += a[q];
+                }
+                reinterpret_cast<uint4 *>(y + row * P.ldy + col)[v] = Vec<T>::narrow(f);
+            }
+            continue;
+        }
+        const uint4 r = philox4x32_10(make_uint4(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32),
+                                                 static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)),
+                                      k0, k1);
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (i0 + e < P.total) {
+                const uint32_t bits = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu;
+                float f = bits >= P.drop ? to_f32(x[row * P.ldx + col]) * P.scale : 0.f;
+                if (res) f += to_f32(res[row * P.ldr + col]);
+                y[row * P.ldy + col] = from_f32<T>(f);
+                if (++col == P.cols) {
+                    col = 0;
+                    ++row;
+                }
+            }
+        }
+    }
+}
+
+template <typename T>
+void launch(const DropoutParams &p, bool vec, int sms, cudaStream_t s) {
+    const int64_t blocks = std::min<int64_t>(ceil_div(ceil_div(p.total, 8), 256), int64_t(sms) * 32);
+    const unsigned grid = static_cast<unsigned>(blocks);
+    if (vec) dropout_kernel<T, true><<<grid, 256, 0, s>>>(p);
+    else dropout_kernel<T, false><<<grid, 256, 0, s>>>(p);
+}
+
+mqc_status dropout(const char *name, const void *x, int64_t ldx, const void *res, int64_t ldr, int64_t rows,
+                   int64_t cols, int32_t dtype, double p, uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
+                   void *y, int64_t ldy, void *stream) {
+    if (dtype != MQC_F32 && dtype != MQC_BF16 && dtype != MQC_F16) return fail(MQC_ERR_INVALID, "%s: bad dtype", name);
+    if (rows < 0 || cols < 0) return fail(MQC_ERR_INVALID, "%s: negative extent", name);
+    if (!(p >= 0.0 && p <= 1.0)) return fail(MQC_ERR_INVALID, "%s: p must be within [0, 1]", name);
+    if (rows == 0 || cols == 0) return MQC_OK;
+    if (x == nullptr || y == nullptr) return fail(MQC_ERR_INVALID, "%s: null tensor", name);
+    const int64_t most = int64_t(1) << 40;
+    if (cols > most || rows > most / cols) return fail(MQC_ERR_INVALID, "%s: tensor too large", name);
+    if (ldx < cols || ldy < cols || (res && ldr < cols) || ldx > most || ldy > most || (res && ldr > most))
+        return fail(MQC_ERR_INVALID, "%s: row stride out of range", name);
+    if (!aligned16(x) || !aligned16(y) || (res && !aligned16(res)))
+        return fail(MQC_ERR_ALIGNMENT, "%s: tensor not 16-byte aligned", name);
+    if ((reinterpret_cast<uintptr_t>(offset_dev) & 7u) != 0)
+        return fail(MQC_ERR_ALIGNMENT, "%s: offset_dev not 8-byte aligned", name);
+    if ((y == x && ldx != ldy) || (res && y == res && ldr != ldy))
+        return fail(MQC_ERR_INVALID, "%s: an output in place needs its input's row stride", name);
+    DeviceLimits d;
+    mqc_status st = device_limits(&d);
+    if (st != MQC_OK) return st;
+    DropoutParams P{};
+    P.x = x;
+    P.res = res;
+    P.y = y;
+    P.ldx = ldx;
+    P.ldr = ldr;
+    P.ldy = ldy;
+    P.cols = cols;
+    P.total = rows * cols;
+    P.seed = seed;
+    P.offset = offset;
+    P.offset_dev = offset_dev;
+    P.drop = static_cast<uint32_t>(std::floor(p * 65536.0 + 0.5));
+    P.scale = P.drop >= 65536u ? 0.f : 65536.f / static_cast<float>(65536u - P.drop);
+    // rows that follow one another are one long row
+    const bool one = rows == 1 || (ldx == cols && ldy == cols && (!res || ldr == cols));
+    if (one) P.cols = P.total;
+    const int64_t per16 = 16 / dtype_bytes(dtype);
+    const bool vec = one || (cols % 8 == 0 && ldx % per16 == 0 && ldy % per16 == 0 && (!res || ldr % per16 == 0));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == MQC_F32) launch<float>(P, vec, d.sms, s);
+    else if (dtype == MQC_BF16) launch<__nv_bfloat16>(P, vec, d.sms, s);
+    else launch<__half>(P, vec, d.sms, s);
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MQC_OK : cuda_fail(e, "dropout_kernel launch");
+}
+
+}  // namespace
+}  // namespace mqc
+
+extern "C" {
+
+mqc_status mqc_dropout_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, int64_t rows, int64_t cols,
+                           int32_t dtype, double p, uint64_t seed, uint64_t offset, const uint64_t *offset_dev,
+                           void *y, int64_t ldy, void *stream) {
+    return mqc::dropout("dropout_fwd", x, ldx, residual, ldr, rows, cols, dtype, p, seed, offset, offset_dev, y, ldy,
+                        stream);
+}
+
+mqc_status mqc_dropout_bwd(const void *g, int64_t ldg, int64_t rows, int64_t cols, int32_t dtype, double p,
+                           uint64_t seed, uint64_t offset, const uint64_t *offset_dev, void *gx, int64_t ldgx,
+                           void *stream) {
+    return mqc::dropout("dropout_bwd", g, ldg, nullptr, 0, rows, cols, dtype, p, seed, offset, offset_dev, gx, ldgx,
+                        stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,43 @@
+// host.h -- host helpers shared by the library's translation units: error
+// reporting, device properties, and the encoder of TMA tensor maps.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/mqc.h"
+
+namespace mqc {
+
+// Records the one-line reason of the calling thread's last failure and
+// returns `s`.
+mqc_status fail(mqc_status s, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
+mqc_status cuda_fail(cudaError_t e, const char *what);
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The current device: its ordinal, SM count and shared memory per block.
+// Fails on anything but sm_100.
+struct DeviceLimits {
+    int device, sms, max_smem;
+};
+mqc_status device_limits(DeviceLimits *out);
+
+// Tensor map of a row-major matrix of 2-byte elements, `rows` x `cols` with
+// row stride `ld` elements: boxes of 64 elements (128 bytes, the 128-byte
+// swizzle) x `box_rows` rows; coordinates are (byte, row).  Bytes beyond the
+// matrix read as zero.  `base` and ld * 2 must be multiples of 16.
+mqc_status encode_matrix_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld,
+                             int box_rows);
+
+// Reads and clears the device error word of the linear kernels (each
+// translation unit has its own word).
+cudaError_t linear_take_device_error(int *value);
+
+inline bool act_ok(int act) { return act >= MQC_ACT_NONE && act <= MQC_ACT_GELU; }
+inline int dtype_bytes(int dtype) { return dtype == MQC_F32 ? 4 : 2; }
+
+}  // namespace mqc

@@ -14,6 +14,7 @@
 
 #include "../../include/mqc.h"
 #include "common.cuh"
+#include "host.h"
 #include "conv_gemm.cuh"
 #include "im2col.cuh"
 #include "quantize.cuh"
@@ -24,8 +25,10 @@
 using namespace mqc;
 
 namespace {
-
 thread_local char g_msg[512] = "";
+}
+
+namespace mqc {
 
 mqc_status fail(mqc_status s, const char *fmt, ...) {
     va_list ap;
@@ -39,10 +42,11 @@ mqc_status cuda_fail(cudaError_t e, const char *what) {
     return fail(MQC_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+}  // namespace mqc
+
+namespace {
+
 int64_t nb32(int64_t x) { return ceil_div(x, 32); }
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool fmt_ok(int f) { return f == MQC_E4M3 || f == MQC_E5M2 || f == MQC_E2M1; }
 bool mx_ok(const mqc_mx *m) {
@@ -221,6 +225,32 @@ mqc_status encode_codes_map(CUtensorMap *map, const void *base, int rank, const 
     }
     return MQC_OK;
 }
+
+}  // namespace
+
+namespace mqc {
+
+mqc_status device_limits(DeviceLimits *out) {
+    DevInfo *d;
+    mqc_status st = dev_info(d);
+    if (st != MQC_OK) return st;
+    out->device = static_cast<int>(d - g_dev);
+    out->sms = d->sms;
+    out->max_smem = d->max_smem;
+    return MQC_OK;
+}
+
+mqc_status encode_matrix_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld,
+                             int box_rows) {
+    const uint64_t dims[2] = {static_cast<uint64_t>(cols) * 2, static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(ld) * 2};
+    const uint32_t box[2] = {128, static_cast<uint32_t>(box_rows)};
+    return encode_codes_map(map, base, 2, dims, strides, box, 4);
+}
+
+}  // namespace mqc
+
+namespace {
 
 int largest_wkb(int64_t nblocks) { return nblocks % 4 == 0 ? 4 : (nblocks % 2 == 0 ? 2 : 1); }
 
@@ -1850,6 +1880,12 @@ mqc_status mqc_get_device_status(void *stream) {
     if (v != 0) {
         e = cudaMemcpyToSymbol(g_mqc_device_error, &zero, sizeof zero);
         if (e != cudaSuccess) return cuda_fail(e, "clear device error word");
+    }
+    int lin = 0;
+    e = linear_take_device_error(&lin);
+    if (e != cudaSuccess) return cuda_fail(e, "linear kernels' device error word");
+    if (v == 0) v = lin;
+    if (v != 0) {
         return fail(MQC_ERR_DEVICE_TIMEOUT, "a kernel-side wait ran out of time (device error %d)", v);
     }
     return MQC_OK;

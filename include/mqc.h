@@ -358,6 +358,135 @@ MQC_API mqc_status mqc_conv2d_bwd_weight_noalloc(const void *gq, const uint8_t *
                                          const void *xq, const uint8_t *xs, const mqc_mx *xf,
                                          const mqc_conv *conv, float *gw, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Dense layers beside the convolutions: group norm with an activation, the
+ * matrix product of a linear layer, and dropout.  (The paper has no
+ * counterpart: its networks keep such layers out of the 8-bit formats.)
+ * Their tensors hold fp32, bf16 or fp16 elements; parameters that are added
+ * or multiplied per channel (gamma, beta, bias), statistics and the gradients
+ * of such parameters are fp32.  Every sum is held in fp32 or more, and a
+ * result is rounded once, to nearest even, when it is stored. */
+typedef enum { MQC_F32 = 0, MQC_BF16 = 1, MQC_F16 = 2 } mqc_dtype;
+
+/* Activation codes beside MQC_ACT_NONE, _RELU and _SILU that the dense layers
+ * take: the exact GELU, x * (1 + erf(x / sqrt 2)) / 2. */
+#define MQC_ACT_GELU 3
+
+/* Group norm with an activation, channels last:
+ *   mean[n][j], var[n][j] over the D = C/groups channels of group j and all
+ *   H*W pixels of image n (var is the mean squared deviation),
+ *   rstd = 1 / sqrt(var + eps),
+ *   z = (x - mean) * rstd * gamma[c] + beta[c],   y = act(z).
+ * The deviations are taken from the mean, never from the mean of squares, so
+ * a large common offset costs no precision.
+ *   x, y    [N][C][H][W] tensors of `dtype`, described by xd and yd (d0 = N,
+ *           d1 = C, d2 = H, d3 = W) in elements: element stride 1 along the
+ *           channels, and rows of pixels that follow one another (s2 = d3 *
+ *           s3, any s3 >= C; any s0), else MQC_ERR_UNSUPPORTED.  y may be x
+ *           itself (same descriptor); partial overlap is not allowed.
+ *   gamma, beta   fp32 [C]; NULL stands for ones / zeros.
+ *   groups  divides C.      eps >= 0.     act  MQC_ACT_*, GELU included.
+ *   mean, rstd    fp32 [N][groups], written (the backward pass reads them).
+ *   workspace     at least mqc_group_norm_workspace_bytes() bytes of scratch.
+ * N = 0 writes nothing and succeeds; C, H and W are at least 1.
+ * Errors: MQC_ERR_INVALID, MQC_ERR_UNSUPPORTED, MQC_ERR_ALIGNMENT,
+ * MQC_ERR_WORKSPACE, MQC_ERR_CUDA. */
+MQC_API mqc_status mqc_group_norm_fwd(const void *x, const mqc_t4 *xd, int32_t dtype, const float *gamma,
+                              const float *beta, int32_t groups, float eps, int32_t act, void *y, const mqc_t4 *yd,
+                              float *mean, float *rstd, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Gradients of the above.  With xhat = (x - mean) * rstd, z recomputed from
+ * it, dz = g * act'(z):
+ *   ggamma[c] = sum dz * xhat,   gbeta[c] = sum dz   (over images and pixels)
+ *   gx = rstd * (gamma dz - (S1 + xhat S2) / (D H W)),
+ *   S1 = sum gamma dz,  S2 = sum gamma dz xhat   over the group.
+ * act' of ReLU at 0 is 0.
+ *   g, x, gx   tensors of `dtype`, each with its own descriptor (as above, the
+ *           same extents).  gx may be g or x itself (same descriptor).
+ *   mean, rstd   as mqc_group_norm_fwd wrote them.
+ *   ggamma, gbeta   fp32 [C], overwritten; either may be NULL.  N = 0 writes
+ *           zeros.  The sums are taken in a fixed order.
+ * Errors: as mqc_group_norm_fwd. */
+MQC_API mqc_status mqc_group_norm_bwd(const void *g, const mqc_t4 *gd, const void *x, const mqc_t4 *xd, int32_t dtype,
+                              const float *gamma, const float *beta, const float *mean, const float *rstd,
+                              int32_t groups, int32_t act, void *gx, const mqc_t4 *gxd, float *ggamma,
+                              float *gbeta, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch of both directions for tensors of these extents. */
+MQC_API size_t mqc_group_norm_workspace_bytes(const mqc_t4 *xd, int32_t dtype, int32_t groups);
+
+/* One linear layer: M rows (tokens, pixels) of K features to N features.
+ * Every matrix is row-major with its own row stride in elements (at least
+ * its number of columns); `dtype` is MQC_BF16 or MQC_F16 (MQC_F32 is
+ * MQC_ERR_UNSUPPORTED: the tensor cores have no fp32 operands). */
+typedef struct {
+    int32_t M, N, K;
+    int32_t dtype, act;
+    int64_t ldx, ldw;            /* x [M][K], w [N][K] */
+    int64_t ldr, ldy, ldz;       /* residual, y and z [M][N] (forward; z also backward) */
+    int64_t ldg, ldgx, ldgw;     /* g [M][N], gx [M][K], gw [N][K] (backward) */
+} mqc_linear;
+
+/* Forward: z = x . w^T + bias, y = act(z) + residual.
+ *   bias      fp32 [N], or NULL.
+ *   residual  [M][N] of `dtype`, or NULL.  It may be y itself (same stride).
+ *   z         [M][N] of `dtype`, or NULL: the pre-activation, rounded, for the
+ *             backward pass.  y is computed from the unrounded z.
+ *   workspace at least mqc_linear_fwd_workspace_bytes() bytes (0 when the rows
+ *             of x and w are multiples of 16 bytes; else their padded copies).
+ * Products are exact and summed in fp32 on the tensor cores.  y and z must
+ * not overlap x, w or each other.  M = 0 succeeds and writes nothing; N and K
+ * are at least 1.  The strides that an absent matrix would have are ignored.
+ * Errors: MQC_ERR_INVALID, MQC_ERR_UNSUPPORTED, MQC_ERR_ALIGNMENT,
+ * MQC_ERR_WORKSPACE, MQC_ERR_CUDA. */
+MQC_API mqc_status mqc_linear_fwd(const mqc_linear *lin, const void *x, const void *w, const float *bias,
+                          const void *residual, void *y, void *z, void *workspace, size_t workspace_bytes,
+                          void *stream);
+MQC_API size_t mqc_linear_fwd_workspace_bytes(const mqc_linear *lin);
+
+/* Backward: dz = g * act'(z), gx = dz . w, gw = dz^T . x, gb = sum of dz over
+ * the rows (the residual's gradient is g itself).
+ *   z         what the forward pass wrote; NULL (and ignored) for
+ *             MQC_ACT_NONE.  act' of ReLU at 0 is 0.
+ *   gx, gw    of `dtype`, gb fp32 [N]; each may be NULL (not computed).  x is
+ *             only read for gw, w only for gx; each may be NULL otherwise.
+ *   workspace at least mqc_linear_bwd_workspace_bytes() bytes.
+ * dz enters the two products rounded to `dtype` (the tensor cores' operand
+ * type); gb is summed from the unrounded dz.  M = 0 writes zeros to gw and
+ * gb.  Outputs must not overlap inputs or each other.  The same inputs give
+ * the same bits.
+ * Errors: as mqc_linear_fwd. */
+MQC_API mqc_status mqc_linear_bwd(const mqc_linear *lin, const void *g, const void *z, const void *x, const void *w,
+                          void *gx, void *gw, float *gb, void *workspace, size_t workspace_bytes, void *stream);
+MQC_API size_t mqc_linear_bwd_workspace_bytes(const mqc_linear *lin);
+
+/* Dropout from a counter-based generator; the mask is never stored:
+ *   y = (keep ? x * 65536 / (65536 - t) : 0) + residual,   keep = r >= t,
+ * t = p * 65536 rounded to the nearest integer (the drop probability is
+ * t / 65536 and the scale matches it exactly; p = 1 drops everything), and r
+ * the 16 random bits of the element.  Element (row, col) has index i = row *
+ * cols + col, whatever the strides; its bits are the half i % 2 of word (i %
+ * 8) / 2 of the Philox4x32-10 block (Salmon et al., SC 2011) with key = the
+ * halves of `seed` and counter = (i / 8 low, i / 8 high, offset low, offset
+ * high).
+ *   x, y, residual   [rows][cols] of `dtype`, row strides ldx, ldy, ldr in
+ *           elements; residual may be NULL.  y may be x or residual itself
+ *           (same stride).
+ *   offset  plus, when offset_dev is not NULL, the device value *offset_dev
+ *           (8-byte aligned, read when the kernel runs): a captured graph
+ *           draws new bits at every replay when the program advances it.
+ * rows or cols = 0 succeeds and writes nothing.
+ * Errors: MQC_ERR_INVALID, MQC_ERR_ALIGNMENT, MQC_ERR_CUDA. */
+MQC_API mqc_status mqc_dropout_fwd(const void *x, int64_t ldx, const void *residual, int64_t ldr, int64_t rows,
+                           int64_t cols, int32_t dtype, double p, uint64_t seed, uint64_t offset,
+                           const uint64_t *offset_dev, void *y, int64_t ldy, void *stream);
+
+/* Its gradient: gx = keep ? g * 65536 / (65536 - t) : 0 with the same bits
+ * (the residual's gradient is g itself).  Same arguments and errors. */
+MQC_API mqc_status mqc_dropout_bwd(const void *g, int64_t ldg, int64_t rows, int64_t cols, int32_t dtype, double p,
+                           uint64_t seed, uint64_t offset, const uint64_t *offset_dev, void *gx, int64_t ldgx,
+                           void *stream);
+
 /* Synchronizes `stream`, then reads and clears the device error flag set by a
  * bounded wait that ran out.  MQC_OK if none; MQC_ERR_DEVICE_TIMEOUT if one
  * did; MQC_ERR_CUDA if the synchronization itself failed. */
