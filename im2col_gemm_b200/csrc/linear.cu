@@ -34,13 +34,13 @@ struct Epilogue {
     int act = MQC_ACT_NONE;
 };
 
-template <typename T>
-mqc_status set_smem(int device, int bytes) {
-    static std::atomic<bool> done[64];
-    if (done[device].load(std::memory_order_acquire)) return MQC_OK;
-    cudaError_t e = cudaFuncSetAttribute(linear_tile_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear_tile_kernel)");
-    done[device].store(true, std::memory_order_release);
+// Dynamic shared memory of a kernel, allowed once per device.
+mqc_status allow_smem(const void *kernel, int index, const DeviceLimits &d) {
+    static std::atomic<bool> done[4][64];
+    if (done[index][d.device].load(std::memory_order_acquire)) return MQC_OK;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, d.max_smem - 2048);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(linear kernel)");
+    done[index][d.device].store(true, std::memory_order_release);
     return MQC_OK;
 }
 
@@ -49,6 +49,7 @@ mqc_status set_smem(int device, int bytes) {
 mqc_status launch_product(Operand X, Operand W, int32_t tokens, int32_t features, int32_t red, int32_t dtype,
                           const Epilogue &E, const DeviceLimits &d, cudaStream_t stream) {
     LinParams P;
+    const bool bf16 = dtype == MQC_BF16;
     // few tokens: the features fill the 128 rows of the tensor core's tile
     // and the tokens its columns, so that no rows are spent on padding
     P.swap = tokens <= 64;
@@ -58,26 +59,60 @@ mqc_status launch_product(Operand X, Operand W, int32_t tokens, int32_t features
     P.R = red;
     P.a_mn = A.mn;
     P.b_mn = B.mn;
-    P.tiles_i = static_cast<int32_t>(ceil_div(P.I, kLinRows));
-    const int nkb = static_cast<int>(ceil_div(red, kLinBK));
-    // the widest column tile that still gives every SM one; all the tokens of
-    // the swapped form in one tile, so that the weights are read once
-    if (P.swap) {
-        P.bn = static_cast<int32_t>(round_up(P.J, 16));
-    } else {
-        P.bn = 256;
-        while (P.bn > 32 && (P.bn / 2 >= P.J || P.tiles_i * ceil_div(P.J, P.bn) < d.sms)) P.bn /= 2;
-    }
-    const int64_t tiles = P.tiles_i * ceil_div(P.J, P.bn);
     P.splits = 1;
-    while (P.splits < 8 && tiles * P.splits < d.sms && nkb / (2 * P.splits) >= 2) P.splits *= 2;
-    P.b_bytes = (P.b_mn ? static_cast<int>(round_up(P.bn, 64)) : P.bn) * kLinBK * 2;
-    const int stage = kLinRows * kLinBK * 2 + P.b_bytes;
-    const int part = P.swap ? P.bn * kLinRows * 4 : kLinRows * (P.bn + 1) * 4;
-    const int room = (d.max_smem - 2048) / (tiles * P.splits > d.sms && P.bn <= 64 ? 2 : 1) - 1024;
-    P.stages = std::max(1, std::min({kLinMaxStages, room / stage, static_cast<int>(ceil_div(nkb, P.splits))}));
-    const int smem = 1024 + std::max(P.stages * stage, part);
-    P.idesc = make_idesc_f16(dtype == MQC_BF16, P.a_mn, P.b_mn, kLinRows, P.bn);
+    const int nkb = static_cast<int>(ceil_div(red, kLinBK));
+    const int room = d.max_smem - 2048 - 1024;
+    int64_t grid;
+    int cluster, threads, smem, a_rows, b_rows;
+    // CTA pairs once their 256-row tiles fill most of the SM pairs
+    const int64_t pair_rows = ceil_div(P.I, 2 * kLinRows);
+    const int pairs = d.sms / 2;
+    const bool pair = !P.swap && pair_rows * ceil_div(P.J, 128) >= pairs * 3 / 4;
+    if (pair) {
+        // 256 or 128 columns: the fewer rounds of tiles, a narrow tile counted
+        // as 0.6 of a wide one
+        const int64_t wide = ceil_div(pair_rows * ceil_div(P.J, 256), pairs) * 10;
+        const int64_t narrow = ceil_div(pair_rows * ceil_div(P.J, 128), pairs) * 6;
+        P.bn = narrow < wide ? 128 : 256;
+        P.tiles_i = static_cast<int32_t>(pair_rows);
+        P.b_bytes = P.bn / 2 * kLinBK * 2;
+        const int64_t tiles = pair_rows * ceil_div(P.J, P.bn);
+        const int stage = kLinRows * kLinBK * 2 + P.b_bytes;
+        P.stages = std::min(kPairMaxStages, room / stage);
+        smem = 1024 + P.stages * stage;
+        grid = 2 * std::min<int64_t>(tiles, pairs);
+        if (tiles > (int64_t(1) << 30)) return fail(MQC_ERR_INVALID, "linear: too many tiles");
+        P.idesc = make_idesc_f16(bf16, P.a_mn, P.b_mn, 2 * kLinRows, P.bn);
+        cluster = 2;
+        threads = kPairThreads;
+        a_rows = kLinRows;
+        b_rows = P.bn / 2;
+    } else {
+        P.tiles_i = static_cast<int32_t>(ceil_div(P.I, kLinRows));
+        // the widest column tile that still gives every SM one; all the tokens
+        // of the swapped form in one tile, so that the weights are read once
+        if (P.swap) {
+            P.bn = static_cast<int32_t>(round_up(P.J, 16));
+        } else {
+            P.bn = 256;
+            while (P.bn > 32 && (P.bn / 2 >= P.J || P.tiles_i * ceil_div(P.J, P.bn) < d.sms)) P.bn /= 2;
+        }
+        const int64_t tiles = P.tiles_i * ceil_div(P.J, P.bn);
+        while (P.splits < 8 && tiles * P.splits < d.sms && nkb / (2 * P.splits) >= 2) P.splits *= 2;
+        P.b_bytes = (P.b_mn ? static_cast<int>(round_up(P.bn, 64)) : P.bn) * kLinBK * 2;
+        const int stage = kLinRows * kLinBK * 2 + P.b_bytes;
+        const int part = P.swap ? P.bn * kLinRows * 4 : kLinRows * (P.bn + 1) * 4;
+        const int share = tiles * P.splits > d.sms && P.bn <= 64 ? room / 2 - 512 : room;
+        P.stages = std::max(1, std::min({kLinMaxStages, share / stage, static_cast<int>(ceil_div(nkb, P.splits))}));
+        smem = 1024 + std::max(P.stages * stage, part);
+        grid = tiles * P.splits;
+        if (grid > (int64_t(1) << 31) - 1) return fail(MQC_ERR_INVALID, "linear: too many tiles");
+        P.idesc = make_idesc_f16(bf16, P.a_mn, P.b_mn, kLinRows, P.bn);
+        cluster = P.splits;
+        threads = kLinThreads;
+        a_rows = kLinRows;
+        b_rows = P.bn;
+    }
     P.act = E.act;
     P.bias = E.bias;
     P.res = E.res;
@@ -87,30 +122,28 @@ mqc_status launch_product(Operand X, Operand W, int32_t tokens, int32_t features
     P.ldy = E.ldy;
     P.ldz = E.ldz;
     mqc_status st = A.mn ? encode_matrix_map(&P.amap, A.p, red, P.I, A.ld, kLinBK)
-                         : encode_matrix_map(&P.amap, A.p, P.I, red, A.ld, kLinRows);
+                         : encode_matrix_map(&P.amap, A.p, P.I, red, A.ld, a_rows);
     if (st != MQC_OK) return st;
     st = B.mn ? encode_matrix_map(&P.bmap, B.p, red, P.J, B.ld, kLinBK)
-              : encode_matrix_map(&P.bmap, B.p, P.J, red, B.ld, P.bn);
+              : encode_matrix_map(&P.bmap, B.p, P.J, red, B.ld, b_rows);
     if (st != MQC_OK) return st;
-    if (tiles * P.splits > (int64_t(1) << 31) - 1) return fail(MQC_ERR_INVALID, "linear: too many tiles");
-    st = dtype == MQC_BF16 ? set_smem<__nv_bfloat16>(d.device, d.max_smem - 2048)
-                           : set_smem<__half>(d.device, d.max_smem - 2048);
-    if (st != MQC_OK) return st;
+    void (*kernel)(LinParams) = pair ? (bf16 ? linear_pair_kernel<__nv_bfloat16> : linear_pair_kernel<__half>)
+                                     : (bf16 ? linear_tile_kernel<__nv_bfloat16> : linear_tile_kernel<__half>);
+    if ((st = allow_smem(reinterpret_cast<const void *>(kernel), 2 * pair + bf16, d)) != MQC_OK) return st;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * P.splits));
-    cfg.blockDim = dim3(kLinThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = P.splits;
+    at[0].val.clusterDim.x = cluster;
     at[0].val.clusterDim.y = 1;
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = dtype == MQC_BF16 ? cudaLaunchKernelEx(&cfg, linear_tile_kernel<__nv_bfloat16>, P)
-                                      : cudaLaunchKernelEx(&cfg, linear_tile_kernel<__half>, P);
-    return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear_tile_kernel launch");
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
+    return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear kernel launch");
 }
 
 // Bytes of a padded copy of a rows x cols matrix, and whether one is needed.

@@ -257,6 +257,256 @@ __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_c
     if (P.splits > 1) cluster_sync();   // no CTA leaves while others read its part
 }
 
+// ---------------------------------------------------------------- CTA pairs
+// TMA load into this CTA's shared memory that completes on a barrier of either
+// CTA of the pair (`bar`: shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *map, uint32_t bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_f16_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// One arrival on the barrier at this offset in both CTAs of the pair, when the
+// MMAs issued so far have completed.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+constexpr int kPairThreads = 320;    // warp 0 TMA, warp 1 MMA, warps 2-9 the epilogue
+constexpr int kPairMaxStages = 8;
+
+// bias, activation and residual of 32 consecutive features of one token, in
+// 16-byte accesses (VEC) or element by element with the row's end checked.
+template <typename T, bool VEC>
+__device__ __forceinline__ void lin_store_row(const LinParams &P, const uint32_t (&acc)[32], int64_t m, int n0,
+                                              int N) {
+    const T *res = P.res ? static_cast<const T *>(P.res) + m * P.ldr + n0 : nullptr;
+    T *y = static_cast<T *>(P.y) + m * P.ldy + n0, *z = P.z ? static_cast<T *>(P.z) + m * P.ldz + n0 : nullptr;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(acc[8 * q + e]);
+        if (VEC) {
+            if (P.bias) {
+                const float4 b0 = __ldg(reinterpret_cast<const float4 *>(P.bias + n0) + 2 * q);
+                const float4 b1 = __ldg(reinterpret_cast<const float4 *>(P.bias + n0) + 2 * q + 1);
+                v[0] += b0.x, v[1] += b0.y, v[2] += b0.z, v[3] += b0.w;
+                v[4] += b1.x, v[5] += b1.y, v[6] += b1.z, v[7] += b1.w;
+            }
+            if (z) reinterpret_cast<uint4 *>(z)[q] = Vec<T>::narrow(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = act_value(P.act, v[e]);
+            if (res) {
+                float r[8];
+                Vec<T>::widen(reinterpret_cast<const uint4 *>(res)[q], r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += r[e];
+            }
+            reinterpret_cast<uint4 *>(y)[q] = Vec<T>::narrow(v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (n0 + 8 * q + e < N) lin_store<T>(P, v[e], m, n0 + 8 * q + e);
+        }
+    }
+}
+
+// Large products: a persistent pair of CTAs (one per SM) computes 256 x bn
+// tiles with tcgen05.mma.cta_group::2.  Each CTA holds 128 rows of A and half
+// of B's rows per stage, so an SM reads half the operand bytes from shared
+// memory per product that a lone CTA would; its tensor memory holds two
+// accumulators of 128 x bn, so that the epilogue of one tile runs beside the
+// products of the next.  All full-stage signals go to the first CTA, which
+// issues the products for both.
+template <typename T>
+__global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __grid_constant__ LinParams P) {
+    extern __shared__ uint8_t lin_smem_raw[];
+    __shared__ uint64_t full[kPairMaxStages], empty[kPairMaxStages], acc_full[2], acc_empty[2];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    uint8_t *smem = lin_smem_raw + ((1024u - (smem_u32(lin_smem_raw) & 1023u)) & 1023u);
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const int nkb = (P.R + kLinBK - 1) / kLinBK;
+    const int a_bytes = kLinRows * kLinBK * 2;
+    const int stage_bytes = a_bytes + P.b_bytes;
+    const int tiles_j = (P.J + P.bn - 1) / P.bn, tiles = P.tiles_i * tiles_j;
+    const int step = gridDim.x / 2;
+    volatile int *abort = &abort_flag;
+
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&P.amap);
+        prefetch_tensormap(&P.bmap);
+        for (int s = 0; s < P.stages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 16);   // eight epilogue warps of each CTA
+        }
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    // tile t: bands of eight rows of tiles, column by column inside a band,
+    // so that the tiles in flight share their operands in L2
+    auto place = [&](int t, int &i0, int &j0) {
+        const int band = t / (8 * tiles_j), in = t - band * 8 * tiles_j;
+        const int rows = min(8, P.tiles_i - band * 8);
+        i0 = (band * 8 + in % rows) * 2 * kLinRows;
+        j0 = (in / rows) * P.bn;
+    };
+
+    if (warp == 0) {
+        const bool issuer = elect_one();
+        int s = 0, ph = 0, issued = 0;
+        bool ok = true;
+        for (int t = blockIdx.x / 2; t < tiles && ok; t += step) {
+            int i0, j0;
+            place(t, i0, j0);
+            i0 += rank * kLinRows;
+            j0 += rank * (P.bn / 2);
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (issued >= P.stages && !mbar_wait(&empty[s], ph ^ 1, kLinTimeoutNs, abort)) {
+                    ok = false;
+                    break;
+                }
+                if (issuer) {
+                    uint8_t *a = smem + s * stage_bytes, *b = a + a_bytes;
+                    const uint32_t bar = map_to_rank(smem_u32(&full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * stage_bytes);
+                    if (P.a_mn) {
+                        tma_load_2d_pair(a, &P.amap, bar, i0 * 2, kb * kLinBK);
+                        tma_load_2d_pair(a + 8192, &P.amap, bar, (i0 + 64) * 2, kb * kLinBK);
+                    } else {
+                        tma_load_2d_pair(a, &P.amap, bar, kb * kLinBK * 2, i0);
+                    }
+                    if (P.b_mn) {
+                        for (int j = 0; j < P.b_bytes / 8192; ++j)
+                            tma_load_2d_pair(b + j * 8192, &P.bmap, bar, (j0 + 64 * j) * 2, kb * kLinBK);
+                    } else {
+                        tma_load_2d_pair(b, &P.bmap, bar, kb * kLinBK * 2, j0);
+                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++s == P.stages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        // the last copies land before the shared memory is given up: their
+        // stages are consumed (empty) in the normal course, and given time to
+        // land after a wait that ran out
+        for (int k = 0; k < min(issued, P.stages); ++k) {
+            const int n = issued - 1 - k;
+            mbar_wait(&empty[n % P.stages], (n / P.stages) & 1, *abort ? 100000000ull : kLinTimeoutNs, nullptr);
+        }
+    } else if (warp == 1 && rank == 0) {
+        const bool issuer = elect_one();
+        const uint32_t a_step = P.a_mn ? 2048 : 32, b_step = P.b_mn ? 2048 : 32;
+        int s = 0, ph = 0, n = 0;
+        bool ok = true;
+        for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
+            const int b = n & 1;
+            if (n >= 2 && !mbar_wait(&acc_empty[b], ((n >> 1) & 1) ^ 1, kLinTimeoutNs, abort)) break;
+            tc_fence_after();
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!mbar_wait(&full[s], ph, kLinTimeoutNs, abort)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (issuer) {
+                    const uint32_t a = smem_u32(smem + s * stage_bytes), bs = a + a_bytes;
+#pragma unroll
+                    for (int k = 0; k < kLinBK / 16; ++k) {
+                        const uint64_t ad = make_smem_desc(a + k * a_step, P.a_mn ? 8192 : 16, 1024, kSwizzle128B);
+                        const uint64_t bd = make_smem_desc(bs + k * b_step, P.b_mn ? 8192 : 16, 1024, kSwizzle128B);
+                        tc_mma_f16_pair(tmem + b * P.bn, ad, bd, P.idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                    }
+                    tc_commit_pair(&empty[s]);
+                }
+                __syncwarp();
+                if (++s == P.stages) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+            if (issuer && ok) tc_commit_pair(&acc_full[b]);
+            __syncwarp();
+        }
+    } else if (warp >= 2) {
+        // warps 2-9: a quadrant of the rows, half of the columns
+        const int quad = warp & 3, half = (warp - 2) / 4;
+        const bool vec = P.ldy % 8 == 0 && (!P.res || P.ldr % 8 == 0) && (!P.z || P.ldz % 8 == 0);
+        int n = 0;
+        for (int t = blockIdx.x / 2; t < tiles; t += step, ++n) {
+            const int b = n & 1;
+            if (!mbar_wait(&acc_full[b], (n >> 1) & 1, kLinTimeoutNs, abort)) break;
+            tc_fence_after();
+            int i0, j0;
+            place(t, i0, j0);
+            const int i = i0 + rank * kLinRows + quad * 32 + lane;
+            const int c1 = (half + 1) * (P.bn / 2);
+            for (int c = half * (P.bn / 2); c < c1; c += 32) {
+                uint32_t acc[32];
+                tc_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * P.bn + c, acc);
+                tc_wait_ld();
+                if (c + 32 == c1) {   // read in full: the accumulator may be overwritten
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[b]), 0));
+                }
+                const int j = j0 + c;
+                if (i < P.I && j < P.J) {
+                    if (vec && j + 32 <= P.J) lin_store_row<T, true>(P, acc, i, j, P.J);
+                    else lin_store_row<T, false>(P, acc, i, j, P.J);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
 // Copy of a matrix whose rows are not multiples of 16 bytes into rows of
 // round_up(cols, 8) elements (the tensor maps' stride rule).
 static __global__ void linear_pack_kernel(const uint16_t *src, int64_t ld, int64_t rows, int32_t cols, uint16_t *dst,
