@@ -83,27 +83,77 @@ struct Vec<float> {
     }
 };
 
-// Activations in fp32.  SiLU uses CUDA's fast exponential and division (a
-// relative error of a few 2^-23 where the value matters); GELU the accurate
-// erff.  ReLU passes NaN on.
-__device__ __forceinline__ float act_value(int act, float z) {
-    if (act == MQC_ACT_RELU) return z < 0.f ? 0.f : z;
-    if (act == MQC_ACT_SILU) return __fdividef(z, 1.f + __expf(-z));
-    if (act == MQC_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    return z;
-}
-
-// act'(z).  SiLU: with q = sigmoid(z), q (1 + z (1 - q)); GELU: Phi(z) + z
-// phi(z).
-__device__ __forceinline__ float act_slope(int act, float z) {
-    if (act == MQC_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-    if (act == MQC_ACT_SILU) {
+// Activations in fp32.  ReLU passes NaN on.  SiLU uses CUDA's fast exponential
+// and division (a relative error of a few 2^-23 where the value matters).
+// GELU takes the normal distribution from Abramowitz and Stegun 7.1.26
+// (Handbook of Mathematical Functions, 1964): erfc(x) = t (a1 + ... + a5 t^4)
+// exp(-x^2), t = 1 / (1 + p x), off by at most 1.5e-7: one reciprocal and one
+// exponential without a branch (erff has two ranges, and lanes of both in a
+// warp pay for both).
+struct Relu {
+    __device__ static __forceinline__ float value(float z) { return z < 0.f ? 0.f : z; }
+    __device__ static __forceinline__ float slope(float z) { return z > 0.f ? 1.f : 0.f; }
+};
+struct Silu {
+    __device__ static __forceinline__ float value(float z) { return __fdividef(z, 1.f + __expf(-z)); }
+    // q (1 + z (1 - q)), q = sigmoid(z)
+    __device__ static __forceinline__ float slope(float z) {
         const float q = __fdividef(1.f, 1.f + __expf(-z));
         return q * (1.f + z * (1.f - q));
     }
-    if (act == MQC_ACT_GELU)
-        return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * 0.39894228040143268f * __expf(-0.5f * z * z);
-    return 1.f;
+};
+struct Gelu {
+    // Phi(z), with e = exp(-z^2 / 2)
+    __device__ static __forceinline__ float phi(float z, float e) {
+        const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
+        float c = fmaf(1.061405429f, t, -1.453152027f);
+        c = fmaf(c, t, 1.421413741f);
+        c = fmaf(c, t, -0.284496736f);
+        c = fmaf(c, t, 0.254829592f);
+        c = 0.5f * c * t * e;
+        return z > 0.f ? 1.f - c : c;
+    }
+    __device__ static __forceinline__ float value(float z) { return z * phi(z, __expf(-0.5f * z * z)); }
+    __device__ static __forceinline__ float slope(float z) {
+        const float e = __expf(-0.5f * z * z);
+        return fmaf(z * 0.39894228040143268f, e, phi(z, e));
+    }
+};
+
+// v = act(v); s = act'(z).  One branch for all N elements.
+template <int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
+    if (act == MQC_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = Relu::value(v[i]);
+    } else if (act == MQC_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = Silu::value(v[i]);
+    } else if (act == MQC_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = Gelu::value(v[i]);
+    }
+}
+template <int N>
+__device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (&s)[N]) {
+    if (act == MQC_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = Relu::slope(z[i]);
+    } else if (act == MQC_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = Silu::slope(z[i]);
+    } else if (act == MQC_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = Gelu::slope(z[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[i] = 1.f;
+    }
+}
+__device__ __forceinline__ float act_value(int act, float z) {
+    float v[1] = {z};
+    act_values(act, v);
+    return v[0];
 }
 
 }  // namespace mqc

@@ -193,7 +193,8 @@ __global__ void __launch_bounds__(kGnThreads) gn_apply_kernel(const __grid_const
                 float v[VEC];
                 Pack<T, VEC>::widen(r[u], v);
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) v[q] = act_value(P.act, (v[q] - mean[q]) * a[q] + b[q]);
+                for (int q = 0; q < VEC; ++q) v[q] = (v[q] - mean[q]) * a[q] + b[q];
+                act_values(P.act, v);
                 Pack<T, VEC>::store(y + (p + static_cast<int64_t>(u) * P.ty) * P.op, v);
             }
     }
@@ -232,12 +233,18 @@ __global__ void __launch_bounds__(kGnThreads) gn_bwd_sums_kernel(const __grid_co
                     float xv[VEC], gv[VEC];
                     Pack<T, VEC>::widen(rx[u], xv);
                     Pack<T, VEC>::widen(rg[u], gv);
+                    float z[VEC], sl[VEC];
 #pragma unroll
                     for (int q = 0; q < VEC; ++q) {
-                        const float xh = (xv[q] - mean[q]) * rstd[q];
-                        const float dz = gv[q] * act_slope(P.act, xh * gamma[q] + beta[q]);
+                        xv[q] = (xv[q] - mean[q]) * rstd[q];
+                        z[q] = xv[q] * gamma[q] + beta[q];
+                    }
+                    act_slopes(P.act, z, sl);
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) {
+                        const float dz = gv[q] * sl[q];
                         sa[q] += dz;
-                        sb[q] += dz * xh;
+                        sb[q] += dz * xv[q];
                     }
                 }
         }
@@ -341,12 +348,16 @@ __global__ void __launch_bounds__(kGnThreads) gn_bwd_apply_kernel(const __grid_c
                 float xv[VEC], gv[VEC];
                 Pack<T, VEC>::widen(rx[u], xv);
                 Pack<T, VEC>::widen(rg[u], gv);
+                float z[VEC], sl[VEC];
 #pragma unroll
                 for (int q = 0; q < VEC; ++q) {
-                    const float xh = (xv[q] - mean[q]) * rstd[q];
-                    const float dz = gv[q] * act_slope(P.act, xh * gamma[q] + beta[q]);
-                    xv[q] = rstd[q] * (gamma[q] * dz - k1[q] - xh * k2[q]);
+                    xv[q] = (xv[q] - mean[q]) * rstd[q];
+                    z[q] = xv[q] * gamma[q] + beta[q];
                 }
+                act_slopes(P.act, z, sl);
+#pragma unroll
+                for (int q = 0; q < VEC; ++q)
+                    xv[q] = rstd[q] * (gamma[q] * gv[q] * sl[q] - k1[q] - xv[q] * k2[q]);
                 Pack<T, VEC>::store(o + (p + static_cast<int64_t>(u) * P.ty) * P.op, xv);
             }
     }

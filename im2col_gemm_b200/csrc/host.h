@@ -27,11 +27,11 @@ struct DeviceLimits {
 mqc_status device_limits(DeviceLimits *out);
 
 // Tensor map of a row-major matrix of 2-byte elements, `rows` x `cols` with
-// row stride `ld` elements: boxes of 64 elements (128 bytes, the 128-byte
-// swizzle) x `box_rows` rows; coordinates are (byte, row).  Bytes beyond the
+// row stride `ld` elements: boxes of `box_bytes` (128 or 64, with the swizzle
+// of that width) x `box_rows` rows; coordinates are (byte, row).  Bytes beyond the
 // matrix read as zero.  `base` and ld * 2 must be multiples of 16.
 mqc_status encode_matrix_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld,
-                             int box_rows);
+                             int box_rows, int box_bytes = 128);
 
 // Reads and clears the device error word of the linear kernels (each
 // translation unit has its own word).

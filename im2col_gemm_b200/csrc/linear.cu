@@ -78,8 +78,8 @@ mqc_status launch_product(Operand X, Operand W, int32_t tokens, int32_t features
         P.b_bytes = P.bn / 2 * kLinBK * 2;
         const int64_t tiles = pair_rows * ceil_div(P.J, P.bn);
         const int stage = kLinRows * kLinBK * 2 + P.b_bytes;
-        P.stages = std::min(kPairMaxStages, room / stage);
-        smem = 1024 + P.stages * stage;
+        P.stages = std::min(kPairMaxStages, (room - kPairStaging) / stage);
+        smem = 1024 + P.stages * stage + kPairStaging;
         grid = 2 * std::min<int64_t>(tiles, pairs);
         if (tiles > (int64_t(1) << 30)) return fail(MQC_ERR_INVALID, "linear: too many tiles");
         P.idesc = make_idesc_f16(bf16, P.a_mn, P.b_mn, 2 * kLinRows, P.bn);
@@ -113,6 +113,7 @@ mqc_status launch_product(Operand X, Operand W, int32_t tokens, int32_t features
         a_rows = kLinRows;
         b_rows = P.bn;
     }
+    P.tma_out = pair && E.ldy % 8 == 0 && (!E.z || E.ldz % 8 == 0) && (!E.res || E.ldr % 8 == 0);
     P.act = E.act;
     P.bias = E.bias;
     P.res = E.res;
@@ -127,6 +128,11 @@ mqc_status launch_product(Operand X, Operand W, int32_t tokens, int32_t features
     st = B.mn ? encode_matrix_map(&P.bmap, B.p, red, P.J, B.ld, kLinBK)
               : encode_matrix_map(&P.bmap, B.p, P.J, red, B.ld, b_rows);
     if (st != MQC_OK) return st;
+    if (P.tma_out) {
+        st = encode_matrix_map(&P.ymap, E.y, P.I, P.J, E.ldy, 32, 64);
+        if (st == MQC_OK && E.z) st = encode_matrix_map(&P.zmap, E.z, P.I, P.J, E.ldz, 32, 64);
+        if (st != MQC_OK) return st;
+    }
     void (*kernel)(LinParams) = pair ? (bf16 ? linear_pair_kernel<__nv_bfloat16> : linear_pair_kernel<__half>)
                                      : (bf16 ? linear_tile_kernel<__nv_bfloat16> : linear_tile_kernel<__half>);
     if ((st = allow_smem(reinterpret_cast<const void *>(kernel), 2 * pair + bf16, d)) != MQC_OK) return st;

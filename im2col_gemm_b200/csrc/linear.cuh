@@ -26,6 +26,7 @@ constexpr uint64_t kLinTimeoutNs = 4000000000ull;
 
 struct LinParams {
     CUtensorMap amap, bmap;
+    CUtensorMap ymap, zmap;          // CTA pairs with 16-byte output rows: boxes of 32 x 32 elements
     int32_t I, J, R;                 // extents of A's rows, B's rows and the reduction
     int32_t a_mn, b_mn;              // operand stored with its own index innermost
     int32_t swap;                    // i is the feature and j the token (else i the token)
@@ -34,6 +35,7 @@ struct LinParams {
     int32_t b_bytes;                 // bytes of B per stage
     uint32_t idesc;
     int32_t act;
+    int32_t tma_out;                 // y (and z) leave through their maps
     const float *bias;               // per feature
     const void *res;
     void *y, *z;
@@ -291,42 +293,111 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
 constexpr int kPairThreads = 320;    // warp 0 TMA, warp 1 MMA, warps 2-9 the epilogue
 constexpr int kPairMaxStages = 8;
 
-// bias, activation and residual of 32 consecutive features of one token, in
-// 16-byte accesses (VEC) or element by element with the row's end checked.
-template <typename T, bool VEC>
-__device__ __forceinline__ void lin_store_row(const LinParams &P, const uint32_t (&acc)[32], int64_t m, int n0,
-                                              int N) {
-    const T *res = P.res ? static_cast<const T *>(P.res) + m * P.ldr + n0 : nullptr;
-    T *y = static_cast<T *>(P.y) + m * P.ldy + n0, *z = P.z ? static_cast<T *>(P.z) + m * P.ldz + n0 : nullptr;
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+                 "r"(src), "r"(c0), "r"(c1)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+constexpr int kPairBuf = 2048;       // one 32 x 32 block of 16-bit outputs
+constexpr int kPairStaging = 8 * 2 * kPairBuf;
+
+// The epilogue of one warp: 32 tokens (one a lane) x 32 features.  A lane
+// stores its 64 bytes of y (and z) to a shared-memory block in the 64-byte
+// swizzle of the output's tensor map, which the TMA writes out as whole
+// sectors, clipped at the matrix's last row and (to 16 bytes) its last column.  (Stores of 16 bytes a lane straight
+// to global memory, rows apart, were half sectors: with z they cost 40 us of
+// 221 at 8192 x 4096 x 4096.)
+template <typename T>
+struct PairEpilogue {
+    const LinParams &P;
+    uint8_t *buf;                    // two blocks
+    int lane, turn = 0;
+    __device__ PairEpilogue(const LinParams &p, uint8_t *b, int l) : P(p), buf(b), lane(l) {}
+
+    __device__ __forceinline__ void send(const CUtensorMap *map, const float (&v)[32], int m, int n) {
+        uint8_t *dst = buf + turn * kPairBuf;
+        turn ^= 1;
+        // this block's last copy has been read (the other one's may be running)
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+        __syncwarp();
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        float v[8];
+        for (int q = 0; q < 4; ++q) {
+            const float e[8] = {v[8 * q],     v[8 * q + 1], v[8 * q + 2], v[8 * q + 3],
+                                v[8 * q + 4], v[8 * q + 5], v[8 * q + 6], v[8 * q + 7]};
+            *reinterpret_cast<uint4 *>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) = Vec<T>::narrow(e);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) tma_store_2d(map, smem_u32(dst), n * 2, m);
+        __syncwarp();
+    }
+
+    // The lane's 64 bytes of the residual; elements past the row's end are
+    // not read.
+    __device__ __forceinline__ void fetch(uint4 (&r)[4], int64_t m, int n) const {
+        const T *res = static_cast<const T *>(P.res) + m * P.ldr + n;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(acc[8 * q + e]);
-        if (VEC) {
-            if (P.bias) {
-                const float4 b0 = __ldg(reinterpret_cast<const float4 *>(P.bias + n0) + 2 * q);
-                const float4 b1 = __ldg(reinterpret_cast<const float4 *>(P.bias + n0) + 2 * q + 1);
-                v[0] += b0.x, v[1] += b0.y, v[2] += b0.z, v[3] += b0.w;
-                v[4] += b1.x, v[5] += b1.y, v[6] += b1.z, v[7] += b1.w;
+        for (int q = 0; q < 4; ++q) {
+            r[q] = make_uint4(0, 0, 0, 0);
+            if (m < P.I && n + 8 * q + 8 <= P.J) {
+                r[q] = reinterpret_cast<const uint4 *>(res)[q];
+            } else if (m < P.I) {
+                float e[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) e[k] = n + 8 * q + k < P.J ? to_f32(res[8 * q + k]) : 0.f;
+                r[q] = Vec<T>::narrow(e);
             }
-            if (z) reinterpret_cast<uint4 *>(z)[q] = Vec<T>::narrow(v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = act_value(P.act, v[e]);
-            if (res) {
-                float r[8];
-                Vec<T>::widen(reinterpret_cast<const uint4 *>(res)[q], r);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += r[e];
-            }
-            reinterpret_cast<uint4 *>(y)[q] = Vec<T>::narrow(v);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (n0 + 8 * q + e < N) lin_store<T>(P, v[e], m, n0 + 8 * q + e);
         }
     }
-}
+
+    __device__ __forceinline__ void block(const uint32_t (&acc)[32], const uint4 (&r)[4], int m0, int n) {
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(acc[e]);
+        if (P.bias) {
+            if (n + 32 <= P.J) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float4 b = __ldg(reinterpret_cast<const float4 *>(P.bias + n) + q);
+                    v[4 * q] += b.x, v[4 * q + 1] += b.y, v[4 * q + 2] += b.z, v[4 * q + 3] += b.w;
+                }
+            } else {
+                const float b = n + lane < P.J ? __ldg(P.bias + n + lane) : 0.f;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] += __shfl_sync(0xFFFFFFFFu, b, e);
+            }
+        }
+        if (P.z) send(&P.zmap, v, m0, n);
+        act_values(P.act, v);
+        if (P.res) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float f[8];
+                Vec<T>::widen(r[q], f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[8 * q + e] += f[e];
+            }
+        }
+        send(&P.ymap, v, m0, n);
+    }
+
+    // Output rows of other strides: the accumulators change lanes through
+    // shared memory (fp32, a row's elements rotated by its number, so that
+    // neither side meets bank conflicts) and a warp writes 32 features of one
+    // token at a time.
+    __device__ __forceinline__ void block_any(const uint32_t (&acc)[32], int64_t m0, int n) {
+        float *f = reinterpret_cast<float *>(buf);
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) f[lane * 32 + (e ^ lane)] = __uint_as_float(acc[e]);
+        __syncwarp();
+        if (n + lane < P.J)
+            for (int e = 0; e < 32 && m0 + e < P.I; ++e) lin_store<T>(P, f[e * 32 + (lane ^ e)], m0 + e, n + lane);
+    }
+};
 
 // Large products: a persistent pair of CTAs (one per SM) computes 256 x bn
 // tiles with tcgen05.mma.cta_group::2.  Each CTA holds 128 rows of A and half
@@ -470,32 +541,41 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
     } else if (warp >= 2) {
         // warps 2-9: a quadrant of the rows, half of the columns
         const int quad = warp & 3, half = (warp - 2) / 4;
-        const bool vec = P.ldy % 8 == 0 && (!P.res || P.ldr % 8 == 0) && (!P.z || P.ldz % 8 == 0);
+        PairEpilogue<T> out(P, smem + P.stages * stage_bytes + (warp - 2) * 2 * kPairBuf, lane);
         int n = 0;
         for (int t = blockIdx.x / 2; t < tiles; t += step, ++n) {
             const int b = n & 1;
-            if (!mbar_wait(&acc_full[b], (n >> 1) & 1, kLinTimeoutNs, abort)) break;
-            tc_fence_after();
             int i0, j0;
             place(t, i0, j0);
-            const int i = i0 + rank * kLinRows + quad * 32 + lane;
-            const int c1 = (half + 1) * (P.bn / 2);
-            for (int c = half * (P.bn / 2); c < c1; c += 32) {
+            i0 += rank * kLinRows + quad * 32;
+            j0 += half * (P.bn / 2);
+            uint4 r[4];
+            if (P.res && P.tma_out) out.fetch(r, i0 + lane, j0);
+            if (!mbar_wait(&acc_full[b], (n >> 1) & 1, kLinTimeoutNs, abort)) break;
+            tc_fence_after();
+            for (int c = 0; c < P.bn / 2; c += 32) {
                 uint32_t acc[32];
-                tc_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * P.bn + c, acc);
+                tc_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * P.bn + half * (P.bn / 2) + c,
+                                 acc);
                 tc_wait_ld();
-                if (c + 32 == c1) {   // read in full: the accumulator may be overwritten
+                const bool last = c + 32 == P.bn / 2;
+                if (last) {   // read in full: the accumulator may be overwritten
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[b]), 0));
                 }
-                const int j = j0 + c;
-                if (i < P.I && j < P.J) {
-                    if (vec && j + 32 <= P.J) lin_store_row<T, true>(P, acc, i, j, P.J);
-                    else lin_store_row<T, false>(P, acc, i, j, P.J);
+                if (i0 >= P.I || j0 + c >= P.J) continue;
+                // (a TMA store clips its rows at whole 16 bytes only)
+                if (P.tma_out && (j0 + c + 32 <= P.J || P.J % 8 == 0)) {
+                    uint4 now[4] = {r[0], r[1], r[2], r[3]};
+                    if (P.res && !last) out.fetch(r, i0 + lane, j0 + c + 32);
+                    out.block(acc, now, i0, j0 + c);
+                } else {
+                    out.block_any(acc, i0, j0 + c);
                 }
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncwarp();
     tc_fence_before();
@@ -539,24 +619,22 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(const T *g, int64_t ldg,
     float acc[8] = {};
     if (c0 < N) {
         for (int64_t r = static_cast<int64_t>(blockIdx.y) * slab + ty; r < r1; r += kDzRows) {
-            float v[8];
+            float v[8], zv[8] = {};
             if (VEC && c0 + 8 <= N) {
                 Vec<T>::widen(*reinterpret_cast<const uint4 *>(g + r * ldg + c0), v);
-                if (z) {
-                    float zv[8];
-                    Vec<T>::widen(*reinterpret_cast<const uint4 *>(z + r * ldz + c0), zv);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) v[q] *= act_slope(act, zv[q]);
-                }
+                if (z) Vec<T>::widen(*reinterpret_cast<const uint4 *>(z + r * ldz + c0), zv);
             } else {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    v[q] = 0.f;
-                    if (c0 + q < N) {
-                        v[q] = to_f32(g[r * ldg + c0 + q]);
-                        if (z) v[q] *= act_slope(act, to_f32(z[r * ldz + c0 + q]));
-                    }
+                    v[q] = c0 + q < N ? to_f32(g[r * ldg + c0 + q]) : 0.f;
+                    if (z && c0 + q < N) zv[q] = to_f32(z[r * ldz + c0 + q]);
                 }
+            }
+            if (z) {
+                float s[8];
+                act_slopes(act, zv, s);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] *= s[q];
             }
 #pragma unroll
             for (int q = 0; q < 8; ++q) acc[q] += v[q];

@@ -241,11 +241,11 @@ mqc_status device_limits(DeviceLimits *out) {
 }
 
 mqc_status encode_matrix_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld,
-                             int box_rows) {
+                             int box_rows, int box_bytes) {
     const uint64_t dims[2] = {static_cast<uint64_t>(cols) * 2, static_cast<uint64_t>(rows)};
     const uint64_t strides[1] = {static_cast<uint64_t>(ld) * 2};
-    const uint32_t box[2] = {128, static_cast<uint32_t>(box_rows)};
-    return encode_codes_map(map, base, 2, dims, strides, box, 4);
+    const uint32_t box[2] = {static_cast<uint32_t>(box_bytes), static_cast<uint32_t>(box_rows)};
+    return encode_codes_map(map, base, 2, dims, strides, box, box_bytes / 32);
 }
 
 }  // namespace mqc

@@ -119,7 +119,7 @@ def padded(t, extra, fill=float("nan")):
     return view, whole
 
 
-@pytest.mark.parametrize("shape", [(3, 72, 40), (130, 264, 96), (1500, 1304, 200)])
+@pytest.mark.parametrize("shape", [(3, 72, 40), (130, 264, 96), (1500, 1304, 200), (1500, 1301, 200), (2000, 2045, 67)])
 @pytest.mark.parametrize("extra", [8, 24, 3])
 def test_strides_and_untouched_padding(mqc, shape, extra):
     """Rows with a gap between them (NaN there): inputs give the same bits as
