@@ -3,6 +3,7 @@
 #include "group_norm.cuh"
 
 #include <algorithm>
+#include <atomic>
 
 #include "host.h"
 
@@ -81,30 +82,115 @@ GnTensor tensor_of(const void *p, const mqc_t4 *d) {
     return GnTensor{p, d->d0 > 1 ? d->s0 : 0, d->d3 > 1 ? d->s3 : d->s2};
 }
 
-template <typename T, int VEC>
-void launch_fwd(const GnParams &P, unsigned grid, cudaStream_t s) {
-    gn_stats_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
-    gn_finish_kernel<<<static_cast<unsigned>(ceil_div(int64_t(P.N) * P.G, 4)), 128, 0, s>>>(P);
-    gn_apply_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
+// Shared memory of the on-chip form besides the slots: row sums, 256 partial
+// sums, two channel sums, four group sums, and the slots' alignment.
+int64_t chip_extra(int tx, int ty, int vec, int gpc) {
+    return 16 + 4 * (int64_t(tx) * ty * vec + kGnThreads + 2 * int64_t(tx) * vec + 4 * int64_t(gpc));
+}
+constexpr int64_t kChipSmem = 200 * 1024;
+
+// The on-chip form of a tensor, if a cluster of at most eight CTAs holds one
+// image's chunk of channels: the chunk (whole groups, whole vectors) and the
+// number of CTAs with the least estimated time, in ns: the busiest SM's bytes
+// at its share of the memory bandwidth (43 bytes/ns; rows below 32 bytes waste
+// sectors), and for each round of resident CTAs the latency of loads and
+// barriers, half hidden when several CTAs share an SM.
+bool plan_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
+    const int size = dtype_bytes(dtype);
+    if (vec * size < 4) return false;
+    double best = 1e300;
+    for (int gpc = 1; gpc <= P.G; ++gpc) {
+        if (P.G % gpc != 0 || (int64_t(gpc) * P.D) % vec != 0) continue;
+        const int64_t tx = int64_t(gpc) * P.D / vec;
+        if (tx > kGnThreads) break;
+        const int ty = static_cast<int>(kGnThreads / tx);
+        const int64_t row = int64_t(gpc) * P.D * size;
+        for (int splits = 1; splits <= 8; splits *= 2) {
+            const int64_t slab = ceil_div(P.HW, splits), iters = ceil_div(slab, ty);
+            const int64_t need = iters * tx * ty * vec * size * (bwd ? 2 : 1) +
+                                 chip_extra(static_cast<int>(tx), ty, vec, gpc);
+            if (need > kChipSmem || (splits > 1 && slab * (splits - 1) >= P.HW)) continue;
+            const int64_t ctas = int64_t(P.N) * (P.G / gpc) * splits;
+            const int64_t resident = std::min<int64_t>(4, (228 * 1024) / (need + 1024));
+            const double waste = row < 32 ? 32.0 / row : (row < 64 ? 1.1 : 1.0);
+            const double moved = double(slab) * row * (bwd ? 3 : 2) * waste;
+            const double ns = ceil_div(ctas, 148) * moved / 43.0 +
+                              ceil_div(ctas, 148 * resident) * (resident > 1 ? 1500.0 : 3000.0) + (splits > 1 ? 500.0 : 0.0);
+            if (ns < best) {
+                best = ns;
+                P.gpc = gpc;
+                P.chunks = P.G / gpc;
+                P.tx = static_cast<int32_t>(tx);
+                P.ty = ty;
+                P.splits = splits;
+                P.slab = static_cast<int32_t>(slab);
+                P.iters = static_cast<int32_t>(iters);
+                smem = need;
+            }
+        }
+    }
+    return best < 1e300;
 }
 
 template <typename T, int VEC>
-void launch_bwd(const GnParams &P, unsigned grid, cudaStream_t s) {
-    gn_bwd_sums_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
-    const int64_t gb = ceil_div(int64_t(P.N) * P.G, 4);
+mqc_status launch(GnParams &P, int32_t dtype, bool bwd, const DeviceLimits &d, cudaStream_t s) {
     const int64_t cb = P.ggamma || P.gbeta ? ceil_div(P.C, 32) : 0;
-    gn_bwd_finish_kernel<<<static_cast<unsigned>(gb + cb), 128, 0, s>>>(P, static_cast<int32_t>(gb));
-    gn_bwd_apply_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
+    int64_t smem = 0;
+    if constexpr (VEC * sizeof(T) >= 4)
+        if (plan_chip(P, VEC, dtype, bwd, smem)) {
+            void (*kernel)(GnParams) = bwd ? gn_chip_bwd_kernel<T, VEC> : gn_chip_fwd_kernel<T, VEC>;
+            static std::atomic<bool> allowed[2][64];
+            if (!allowed[bwd][d.device].load(std::memory_order_acquire)) {
+                cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, kChipSmem);
+                if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(group norm)");
+                allowed[bwd][d.device].store(true, std::memory_order_release);
+            }
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(static_cast<unsigned>(int64_t(P.N) * P.chunks * P.splits));
+            cfg.blockDim = dim3(kGnThreads);
+            cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+            cfg.stream = s;
+            cudaLaunchAttribute at[1];
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = P.splits;
+            at[0].val.clusterDim.y = 1;
+            at[0].val.clusterDim.z = 1;
+            cfg.attrs = at;
+            cfg.numAttrs = 1;
+            cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
+            if (e != cudaSuccess) return cuda_fail(e, "group norm launch");
+            if (bwd && cb > 0) {
+                P.slabs = 1;
+                gn_bwd_finish_kernel<<<static_cast<unsigned>(cb), 128, 0, s>>>(P, 0);
+                e = cudaGetLastError();
+                if (e != cudaSuccess) return cuda_fail(e, "group norm launch");
+            }
+            return MQC_OK;
+        }
+    split(P, VEC);
+    const unsigned grid = static_cast<unsigned>(int64_t(P.N) * P.slabs * P.col_blocks);
+    const unsigned gb = static_cast<unsigned>(ceil_div(int64_t(P.N) * P.G, 4));
+    if (bwd) {
+        gn_bwd_sums_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
+        gn_bwd_finish_kernel<<<gb + static_cast<unsigned>(cb), 128, 0, s>>>(P, static_cast<int32_t>(gb));
+        gn_bwd_apply_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
+    } else {
+        gn_stats_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
+        gn_finish_kernel<<<gb, 128, 0, s>>>(P);
+        gn_apply_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
+    }
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MQC_OK : cuda_fail(e, "group norm launch");
 }
 
 template <typename T>
-void launch(const GnParams &P, int vec, bool bwd, unsigned grid, cudaStream_t s) {
-    constexpr int most = 16 / sizeof(T);
-    if constexpr (most == 8)
-        if (vec == 8) return bwd ? launch_bwd<T, 8>(P, grid, s) : launch_fwd<T, 8>(P, grid, s);
-    if (vec == 4) return bwd ? launch_bwd<T, 4>(P, grid, s) : launch_fwd<T, 4>(P, grid, s);
-    if (vec == 2) return bwd ? launch_bwd<T, 2>(P, grid, s) : launch_fwd<T, 2>(P, grid, s);
-    return bwd ? launch_bwd<T, 1>(P, grid, s) : launch_fwd<T, 1>(P, grid, s);
+mqc_status launch_vec(GnParams &P, int vec, int32_t dtype, bool bwd, const DeviceLimits &d, cudaStream_t s) {
+    if constexpr (sizeof(T) == 2)
+        if (vec == 8) return launch<T, 8>(P, dtype, bwd, d, s);
+    if (vec == 4) return launch<T, 4>(P, dtype, bwd, d, s);
+    if (vec == 2) return launch<T, 2>(P, dtype, bwd, d, s);
+    return launch<T, 1>(P, dtype, bwd, d, s);
 }
 
 mqc_status check_workspace(const char *name, const void *ws, size_t bytes, size_t need) {
@@ -115,18 +201,15 @@ mqc_status check_workspace(const char *name, const void *ws, size_t bytes, size_
 }
 
 mqc_status run(const char *name, GnParams &P, int vec, int32_t dtype, bool bwd, cudaStream_t s) {
-    split(P, vec);
-    const int64_t grid = int64_t(P.N) * P.slabs * P.col_blocks;
-    if (grid > (int64_t(1) << 31) - 1 || int64_t(P.N) * P.G > (int64_t(1) << 31))
+    // every grid below has at most this many blocks
+    if (int64_t(P.N) * P.G * 8 > (int64_t(1) << 31) - 1 || int64_t(P.N) * P.C > (int64_t(1) << 31) - 1)
         return fail(MQC_ERR_INVALID, "%s: tensor too large", name);
     DeviceLimits d;
     mqc_status st = device_limits(&d);
     if (st != MQC_OK) return st;
-    if (dtype == MQC_F32) launch<float>(P, vec, bwd, static_cast<unsigned>(grid), s);
-    else if (dtype == MQC_BF16) launch<__nv_bfloat16>(P, vec, bwd, static_cast<unsigned>(grid), s);
-    else launch<__half>(P, vec, bwd, static_cast<unsigned>(grid), s);
-    cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? MQC_OK : cuda_fail(e, "group norm launch");
+    if (dtype == MQC_F32) return launch_vec<float>(P, vec, dtype, bwd, d, s);
+    if (dtype == MQC_BF16) return launch_vec<__nv_bfloat16>(P, vec, dtype, bwd, d, s);
+    return launch_vec<__half>(P, vec, dtype, bwd, d, s);
 }
 
 size_t part_bytes(const mqc_t4 *d, int32_t dtype) {
