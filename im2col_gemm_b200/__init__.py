@@ -35,7 +35,7 @@ EXPORTS = ("mqc_codes_bytes", "mqc_scales_bytes", "mqc_tensor_dims", "mqc_quanti
            "mqc_conv2d_bwd_weight_noalloc", "mqc_conv2d_fwd_workspace_bytes", "mqc_conv2d_bwd_data_workspace_bytes",
            "mqc_quantize_mx_sr", "mqc_conv2d_fwd_quant", "mqc_quantize_mx_batch", "mqc_quantize_nvfp4",
            "mqc_nvfp4_scales_bytes", "mqc_conv2d_fwd_nvfp4", "mqc_group_norm_fwd", "mqc_group_norm_bwd",
-           "mqc_group_norm_workspace_bytes", "mqc_linear_fwd", "mqc_linear_fwd_workspace_bytes", "mqc_linear_bwd",
+           "mqc_group_norm_fwd_workspace_bytes", "mqc_group_norm_bwd_workspace_bytes", "mqc_linear_fwd", "mqc_linear_fwd_workspace_bytes", "mqc_linear_bwd",
            "mqc_linear_bwd_workspace_bytes", "mqc_dropout_fwd", "mqc_dropout_bwd")
 NV_A16, NV_B16, NV_SQ16 = 0, 1, 2
 ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU = 0, 1, 2, 3
@@ -100,7 +100,8 @@ def _load() -> ctypes.CDLL:
         "mqc_group_norm_fwd": (i32, [vp, P(T4), i32, vp, vp, i32, ctypes.c_float, i32, vp, P(T4), vp, vp, vp, sz, vp]),
         "mqc_group_norm_bwd": (i32, [vp, P(T4), vp, P(T4), i32, vp, vp, vp, vp, i32, i32, vp, P(T4), vp, vp, vp, sz,
                                      vp]),
-        "mqc_group_norm_workspace_bytes": (sz, [P(T4), i32, i32]),
+        "mqc_group_norm_fwd_workspace_bytes": (sz, [P(T4), P(T4), i32, i32]),
+        "mqc_group_norm_bwd_workspace_bytes": (sz, [P(T4), P(T4), P(T4), i32, i32]),
         "mqc_linear_fwd": (i32, [P(Linear), vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "mqc_linear_fwd_workspace_bytes": (sz, [P(Linear)]),
         "mqc_linear_bwd": (i32, [P(Linear), vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
@@ -217,8 +218,13 @@ def mqc_group_norm_bwd(g, gd: T4, x, xd: T4, dtype: int, gamma, beta, mean, rstd
                                   act, gx, ctypes.byref(gxd), ggamma, gbeta, workspace, workspace_bytes, stream)
 
 
-def mqc_group_norm_workspace_bytes(xd: T4, dtype: int, groups: int) -> int:
-    return lib.mqc_group_norm_workspace_bytes(ctypes.byref(xd), dtype, groups)
+def mqc_group_norm_fwd_workspace_bytes(xd: T4, yd: T4, dtype: int, groups: int) -> int:
+    return lib.mqc_group_norm_fwd_workspace_bytes(ctypes.byref(xd), ctypes.byref(yd), dtype, groups)
+
+
+def mqc_group_norm_bwd_workspace_bytes(gd: T4, xd: T4, gxd: T4, dtype: int, groups: int) -> int:
+    return lib.mqc_group_norm_bwd_workspace_bytes(ctypes.byref(gd), ctypes.byref(xd), ctypes.byref(gxd), dtype,
+                                                  groups)
 
 
 def mqc_linear_fwd(lin: Linear, x, w, bias, residual, y, z, workspace, workspace_bytes, stream) -> int:
@@ -256,9 +262,15 @@ def mqc_debug_expire_wait(limit_ns: int, stream) -> int:
 
 
 # ------------------------------------------------------------------ torch helpers
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream():
@@ -468,64 +480,83 @@ def conv2d_bwd_weight(gq: Quantized, xq: Quantized, cv: Conv, out=None, workspac
 
 
 # ------------------------------------------------------------------ dense layers
+# These calls can be shorter than the host's work around them, so the helpers
+# pass plain integers to the library and look up no more than they need.
 _DTYPES: dict = {}
+_CUDA: dict = {}
 
 
-def _dtype(t) -> int:
-    if not _DTYPES:
-        torch = _torch()
-        _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{t.dtype} tensors are not supported (float32, bfloat16, float16)")
-    return code
-
-
-def _same(first, *others) -> None:
-    """The other tensors (None: absent) are on the first one's device, of its type."""
-    if not first.is_cuda:
-        raise ValueError("the tensors must be on a CUDA device")
-    for t in others:
-        if t is not None and (t.device != first.device or t.dtype != first.dtype):
-            raise ValueError(f"expected a {first.dtype} tensor on {first.device}, got {t.dtype} on {t.device}")
-
-
-def _params(first, n, *others) -> None:
-    """fp32 parameters or statistics of n contiguous elements on the first tensor's device."""
-    for t in others:
-        if t is not None and (t.device != first.device or t.dtype != _torch().float32 or t.numel() != n
-                              or not t.is_contiguous()):
-            raise ValueError(f"expected {n} contiguous float32 elements on {first.device}, got {tuple(t.shape)} "
-                             f"{t.dtype} on {t.device}")
+def _setup() -> None:
+    torch = _torch()
+    _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _CUDA["stream"] = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _CUDA["count"] = torch.cuda.device_count()
 
 
 def _on_device(fn):
-    """Runs fn with its first tensor's device current, so that the launches and
-    the stream are that device's."""
+    """Runs fn with its first tensor's device current, so that the launches are
+    that device's, and on its current stream (the last argument)."""
     import functools
 
     @functools.wraps(fn)
     def call(t, *args, **kwargs):
-        torch = _torch()
-        if t.is_cuda and t.device.index != torch.cuda.current_device():
-            with torch.cuda.device(t.device):
+        if not t.is_cuda:
+            raise ValueError("the tensors must be on a CUDA device")
+        if not _DTYPES:
+            _setup()
+        device = t.get_device()
+        if _CUDA["count"] > 1 and device != _torch().cuda.current_device():
+            with _torch().cuda.device(device):
                 return fn(t, *args, **kwargs)
         return fn(t, *args, **kwargs)
 
     return call
 
 
-def _scratch(nbytes: int, like, workspace=None):
-    """(tensor or None, its bytes): the caller's workspace, or a new one."""
-    if workspace is not None:
-        return workspace, workspace.numel() * workspace.element_size()
-    return (_torch().empty(nbytes, dtype=_torch().uint8, device=like.device) if nbytes else None), nbytes
+def _dtype(t) -> int:
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{t.dtype} tensors are not supported (float32, bfloat16, float16)")
+    return code
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same(first, *others) -> None:
+    """The other tensors (None: absent) are on the first one's device, of its type."""
+    device, dtype = first.get_device(), first.dtype
+    for t in others:
+        if t is not None and (t.dtype != dtype or t.get_device() != device):
+            raise ValueError(f"expected a {dtype} tensor on {first.device}, got {t.dtype} on {t.device}")
+
+
+def _params(first, n, *others) -> None:
+    """fp32 parameters or statistics of n contiguous elements on the first tensor's device."""
+    for t in others:
+        if t is not None and (_DTYPES.get(t.dtype) != F32 or t.numel() != n or t.get_device() != first.get_device()
+                              or not t.is_contiguous()):
+            raise ValueError(f"expected {n} contiguous float32 elements on {first.device}, got {tuple(t.shape)} "
+                             f"{t.dtype} on {t.device}")
+
+
+def _scratch(nbytes: int, like, workspace):
+    """(tensor or None, address, bytes): the caller's workspace, or a new one."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        torch = _torch()
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        return workspace, workspace.data_ptr(), nbytes
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _image_desc(t, shape) -> T4:
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return T4(*t.shape, *t.stride())
+    return T4(*shape, *t.stride())
 
 
 @_on_device
@@ -534,55 +565,60 @@ def group_norm_fwd(x, groups: int, gamma=None, beta=None, eps: float = 1e-5, act
     """act(group norm of x) for a channels-last tensor x [N][C][H][W] (torch's
     channels_last strides, or any pixel and image strides): (y, mean, rstd),
     mean and rstd fp32 [N][groups] for the backward pass."""
-    torch = _torch()
-    if x.dim() != 4:
+    torch, shape, dt = _torch(), x.shape, _dtype(x)
+    if len(shape) != 4:
         raise ValueError("group_norm_fwd takes [N][C][H][W] tensors")
     _same(x, out)
-    n, c = x.shape[:2]
-    _params(x, c, gamma, beta)
-    xd = _image_desc(x, x.shape)
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device,
+    _params(x, shape[1], gamma, beta)
+    xd = _image_desc(x, shape)
+    y = out if out is not None else torch.empty(shape, dtype=x.dtype, device=x.device,
                                                 memory_format=torch.channels_last)
-    stats = torch.empty((2, n, max(groups, 0)), dtype=torch.float32, device=x.device)
-    dt = _dtype(x)
-    ws, nws = _scratch(mqc_group_norm_workspace_bytes(xd, dt, groups), x, workspace)
-    check(mqc_group_norm_fwd(_ptr(x), xd, dt, _ptr(gamma), _ptr(beta), groups, eps, act, _ptr(y),
-                             _image_desc(y, x.shape), _ptr(stats[0]), _ptr(stats[1]), _ptr(ws), nws, _stream()))
-    return y, stats[0], stats[1]
+    yd = _image_desc(y, shape)
+    mean, rstd = torch.empty((2, shape[0], max(groups, 0)), dtype=torch.float32, device=x.device).unbind(0)
+    ws, at, nws = _scratch(lib.mqc_group_norm_fwd_workspace_bytes(xd, yd, dt, groups), x, workspace)
+    check(lib.mqc_group_norm_fwd(x.data_ptr(), xd, dt, _address(gamma), _address(beta), groups, eps, act, y.data_ptr(),
+                                 yd, mean.data_ptr(), rstd.data_ptr(), at, nws, _CUDA["stream"](x.get_device())))
+    return y, mean, rstd
 
 
 @_on_device
 def group_norm_bwd(g, x, groups: int, mean, rstd, gamma=None, beta=None, act: int = ACT_NONE, out=None,
                    workspace=None):
     """Gradients of group_norm_fwd: (gx, ggamma, gbeta), the last two fp32 [C]."""
-    torch = _torch()
-    if x.dim() != 4:
+    torch, shape, dt = _torch(), x.shape, _dtype(x)
+    if len(shape) != 4:
         raise ValueError("group_norm_bwd takes [N][C][H][W] tensors")
     _same(g, x, out)
-    n, c = x.shape[:2]
-    _params(x, c, gamma, beta)
-    _params(x, n * groups, mean, rstd)
-    xd = _image_desc(x, x.shape)
-    gx = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device,
+    _params(x, shape[1], gamma, beta)
+    _params(x, shape[0] * groups, mean, rstd)
+    gd, xd = _image_desc(g, shape), _image_desc(x, shape)
+    gx = out if out is not None else torch.empty(shape, dtype=x.dtype, device=x.device,
                                                  memory_format=torch.channels_last)
-    sums = torch.empty((2, c), dtype=torch.float32, device=x.device)
-    dt = _dtype(x)
-    ws, nws = _scratch(mqc_group_norm_workspace_bytes(xd, dt, groups), x, workspace)
-    check(mqc_group_norm_bwd(_ptr(g), _image_desc(g, x.shape), _ptr(x), xd, dt, _ptr(gamma), _ptr(beta), _ptr(mean),
-                             _ptr(rstd), groups, act, _ptr(gx), _image_desc(gx, x.shape), _ptr(sums[0]),
-                             _ptr(sums[1]), _ptr(ws), nws, _stream()))
-    return gx, sums[0], sums[1]
+    gxd = _image_desc(gx, shape)
+    ggamma, gbeta = torch.empty((2, shape[1]), dtype=torch.float32, device=x.device).unbind(0)
+    ws, at, nws = _scratch(lib.mqc_group_norm_bwd_workspace_bytes(gd, xd, gxd, dt, groups), x, workspace)
+    check(lib.mqc_group_norm_bwd(g.data_ptr(), gd, x.data_ptr(), xd, dt, _address(gamma), _address(beta),
+                                 mean.data_ptr(), rstd.data_ptr(), groups, act, gx.data_ptr(), gxd, ggamma.data_ptr(),
+                                 gbeta.data_ptr(), at, nws, _CUDA["stream"](x.get_device())))
+    return gx, ggamma, gbeta
 
 
-def _row_stride(t, shape) -> int:
+def _row_stride(t, rows: int, cols: int) -> int:
     """Row stride of a matrix (None: absent) with contiguous rows."""
     if t is None:
-        return shape[1]
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if shape[1] > 1 and t.stride(1) != 1:
+        return cols
+    if t.shape != (rows, cols):
+        raise ValueError(f"expected shape {(rows, cols)}, got {tuple(t.shape)}")
+    row, col = t.stride()
+    if col != 1 and cols > 1:
         raise ValueError("the elements of a row must be contiguous")
-    return t.stride(0) if shape[0] > 1 else max(shape[1], t.stride(0))
+    return row if rows > 1 else max(cols, row)
+
+
+def _linear_sizes(name: str, x, w) -> tuple[int, int, int]:
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError(f"{name} takes x [M][K] and w [N][K], got {tuple(x.shape)} and {tuple(w.shape)}")
+    return x.shape[0], w.shape[0], x.shape[1]
 
 
 @_on_device
@@ -591,18 +627,16 @@ def linear_fwd(x, w, bias=None, act: int = ACT_NONE, residual=None, save_z: bool
     bf16 or fp16 (rows of any stride), bias fp32 [N]; z, the pre-activation for
     the backward pass, with `save_z`, else None."""
     torch = _torch()
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
-        raise ValueError(f"linear_fwd takes x [M][K] and w [N][K], got {tuple(x.shape)} and {tuple(w.shape)}")
+    m, n, k = _linear_sizes("linear_fwd", x, w)
     _same(x, w, residual, out)
-    (m, k), n = x.shape, w.shape[0]
     _params(x, n, bias)
     y = out if out is not None else torch.empty((m, n), dtype=x.dtype, device=x.device)
     z = torch.empty((m, n), dtype=x.dtype, device=x.device) if save_z else None
-    lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, (m, k)), _row_stride(w, (n, k)),
-                 _row_stride(residual, (m, n)), _row_stride(y, (m, n)), n, n, k, k)
-    ws, nws = _scratch(mqc_linear_fwd_workspace_bytes(lin), x, workspace)
-    check(mqc_linear_fwd(lin, _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(z), _ptr(ws), nws,
-                         _stream()))
+    lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, m, k), _row_stride(w, n, k), _row_stride(residual, m, n),
+                 _row_stride(out, m, n), n, n, k, k)
+    ws, at, nws = _scratch(lib.mqc_linear_fwd_workspace_bytes(lin), x, workspace)
+    check(lib.mqc_linear_fwd(lin, x.data_ptr(), w.data_ptr(), _address(bias), _address(residual), y.data_ptr(),
+                             _address(z), at, nws, _CUDA["stream"](x.get_device())))
     return y, z
 
 
@@ -613,45 +647,38 @@ def linear_bwd(g, x, w, z=None, act: int = ACT_NONE, need_x: bool = True, need_w
     forward pass saved it (not read for ACT_NONE).  What is not needed is
     None."""
     torch = _torch()
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
-        raise ValueError(f"linear_bwd takes x [M][K] and w [N][K], got {tuple(x.shape)} and {tuple(w.shape)}")
+    m, n, k = _linear_sizes("linear_bwd", x, w)
     _same(g, x, w, z)
-    (m, k), n = x.shape, w.shape[0]
     gx = torch.empty((m, k), dtype=x.dtype, device=x.device) if need_x else None
     gw = torch.empty((n, k), dtype=x.dtype, device=x.device) if need_w else None
     gb = torch.empty(n, dtype=torch.float32, device=x.device) if need_bias else None
-    lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, (m, k)), _row_stride(w, (n, k)), n, n,
-                 _row_stride(z, (m, n)), _row_stride(g, (m, n)), k, k)
-    ws, nws = _scratch(mqc_linear_bwd_workspace_bytes(lin), x, workspace)
-    check(mqc_linear_bwd(lin, _ptr(g), _ptr(z), _ptr(x), _ptr(w), _ptr(gx), _ptr(gw), _ptr(gb), _ptr(ws), nws,
-                         _stream()))
+    lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, m, k), _row_stride(w, n, k), n, n, _row_stride(z, m, n),
+                 _row_stride(g, m, n), k, k)
+    ws, at, nws = _scratch(lib.mqc_linear_bwd_workspace_bytes(lin), x, workspace)
+    check(lib.mqc_linear_bwd(lin, g.data_ptr(), _address(z), x.data_ptr(), w.data_ptr(), _address(gx), _address(gw),
+                             _address(gb), at, nws, _CUDA["stream"](g.get_device())))
     return gx, gw, gb
 
 
-def _rows_of(t) -> tuple[int, int, int]:
-    """(rows, cols, row stride): a contiguous tensor of any shape is one row."""
-    if t.is_contiguous():
-        return 1, t.numel(), t.numel()
-    if t.dim() != 2:
-        raise ValueError("dropout takes contiguous tensors, or matrices with contiguous rows")
-    return t.shape[0], t.shape[1], _row_stride(t, t.shape)
-
-
 def _dropout_rows(*tensors) -> tuple:
-    """(rows, cols, row strides) common to the tensors (None: absent)."""
-    got = [_rows_of(t) if t is not None else None for t in tensors]
-    if all(r is None or r[0] == 1 for r in got):
-        return got[0][0], got[0][1], [got[0][1]] * len(got)
-    rows, cols = tensors[0].shape
-    return rows, cols, [_row_stride(t, (rows, cols)) for t in tensors]
+    """(rows, cols, row strides) common to the tensors (None: absent);
+    contiguous tensors of any shape are one row."""
+    first = tensors[0]
+    if all(t is None or t.is_contiguous() for t in tensors):
+        n = first.numel()
+        return 1, n, (n,) * len(tensors)
+    if first.dim() != 2:
+        raise ValueError("dropout takes contiguous tensors, or matrices with contiguous rows")
+    rows, cols = first.shape
+    return rows, cols, tuple(_row_stride(t, rows, cols) for t in tensors)
 
 
-def _offset_dev(t, like):
-    if t is None:
-        return None
-    if t.device != like.device or t.dtype != _torch().int64 or t.numel() != 1:
+def _dropout_check(x, other, offset_dev):
+    if other is not None and other.shape != x.shape:
+        raise ValueError(f"expected shape {tuple(x.shape)}, got {tuple(other.shape)}")
+    if offset_dev is not None and (offset_dev.get_device() != x.get_device() or offset_dev.numel() != 1
+                                   or offset_dev.dtype != _torch().int64):
         raise ValueError("offset_dev is one int64 element on the tensor's device")
-    return _ptr(t)
 
 
 @_on_device
@@ -660,29 +687,26 @@ def dropout_fwd(x, p: float, seed: int, offset: int = 0, residual=None, offset_d
     `residual`; the random bits depend on (seed, offset) and the element's
     row-major index alone (mqc_dropout_fwd).  `offset_dev`, an int64 CUDA
     tensor of one element, is added to the offset when the kernel runs."""
-    torch = _torch()
     _same(x, residual, out)
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    for t in (residual, y):
-        if t is not None and t.shape != x.shape:
-            raise ValueError(f"expected shape {tuple(x.shape)}, got {tuple(t.shape)}")
+    _dropout_check(x, residual, offset_dev)
+    if out is not None:
+        _dropout_check(x, out, None)
+    y = out if out is not None else _torch().empty(x.shape, dtype=x.dtype, device=x.device)
     rows, cols, (ldx, ldr, ldy) = _dropout_rows(x, residual, y)
-    check(mqc_dropout_fwd(_ptr(x), ldx, _ptr(residual), ldr, rows, cols, _dtype(x), p, seed, offset,
-                          _offset_dev(offset_dev, x), _ptr(y), ldy, _stream()))
+    check(lib.mqc_dropout_fwd(x.data_ptr(), ldx, _address(residual), ldr, rows, cols, _dtype(x), p, seed, offset,
+                              _address(offset_dev), y.data_ptr(), ldy, _CUDA["stream"](x.get_device())))
     return y
 
 
 @_on_device
 def dropout_bwd(g, p: float, seed: int, offset: int = 0, offset_dev=None, out=None):
     """Gradient of dropout_fwd by x, with the forward call's p, seed and offset."""
-    torch = _torch()
     _same(g, out)
-    gx = out if out is not None else torch.empty(g.shape, dtype=g.dtype, device=g.device)
-    if gx.shape != g.shape:
-        raise ValueError(f"expected shape {tuple(g.shape)}, got {tuple(gx.shape)}")
+    _dropout_check(g, out, offset_dev)
+    gx = out if out is not None else _torch().empty(g.shape, dtype=g.dtype, device=g.device)
     rows, cols, (ldg, ldgx) = _dropout_rows(g, gx)
-    check(mqc_dropout_bwd(_ptr(g), ldg, rows, cols, _dtype(g), p, seed, offset, _offset_dev(offset_dev, g), _ptr(gx),
-                          ldgx, _stream()))
+    check(lib.mqc_dropout_bwd(g.data_ptr(), ldg, rows, cols, _dtype(g), p, seed, offset, _address(offset_dev),
+                              gx.data_ptr(), ldgx, _CUDA["stream"](g.get_device())))
     return gx
 
 

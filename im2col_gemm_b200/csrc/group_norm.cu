@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cstring>
 
 #include "host.h"
 
@@ -63,21 +64,6 @@ void split(GnParams &P, int vec) {
     P.slabs = static_cast<int32_t>(ceil_div(P.HW, P.slab));
 }
 
-// Upper bound over the vector sizes.
-int64_t most_slabs(const mqc_t4 *d, int32_t dtype) {
-    int64_t most = 1;
-    for (int vec = 16 / dtype_bytes(dtype); vec >= 1; vec /= 2) {
-        if (d->d1 % vec != 0) continue;
-        GnParams P{};
-        P.N = d->d0;
-        P.C = d->d1;
-        P.HW = d->d2 * d->d3;
-        split(P, vec);
-        most = std::max<int64_t>(most, P.slabs);
-    }
-    return most;
-}
-
 GnTensor tensor_of(const void *p, const mqc_t4 *d) {
     return GnTensor{p, d->d0 > 1 ? d->s0 : 0, d->d3 > 1 ? d->s3 : d->s2};
 }
@@ -95,7 +81,7 @@ constexpr int64_t kChipSmem = 200 * 1024;
 // at its share of the memory bandwidth (43 bytes/ns; rows below 32 bytes waste
 // sectors), and for each round of resident CTAs the latency of loads and
 // barriers, half hidden when several CTAs share an SM.
-bool plan_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
+bool search_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
     const int size = dtype_bytes(dtype);
     if (vec * size < 4) return false;
     double best = 1e300;
@@ -130,6 +116,56 @@ bool plan_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
         }
     }
     return best < 1e300;
+}
+
+// The same, remembered by sizes (the search takes some microseconds).
+bool plan_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
+    struct Entry {
+        int32_t key[7], plan[7];
+        int64_t smem;
+        bool used, found;
+    };
+    static thread_local Entry cache[16];
+    const int32_t key[7] = {P.N, P.C, P.G, P.HW, vec, dtype, bwd ? 1 : 0};
+    uint32_t h = 2166136261u;
+    for (int32_t k : key) h = (h ^ static_cast<uint32_t>(k)) * 16777619u;
+    Entry &e = cache[(h >> 16) % 16];
+    if (!e.used || memcmp(e.key, key, sizeof key) != 0) {
+        e.found = search_chip(P, vec, dtype, bwd, smem);
+        memcpy(e.key, key, sizeof key);
+        const int32_t plan[7] = {P.gpc, P.chunks, P.tx, P.ty, P.splits, P.slab, P.iters};
+        memcpy(e.plan, plan, sizeof plan);
+        e.smem = smem;
+        e.used = true;
+        return e.found;
+    }
+    P.gpc = e.plan[0];
+    P.chunks = e.plan[1];
+    P.tx = e.plan[2];
+    P.ty = e.plan[3];
+    P.splits = e.plan[4];
+    P.slab = e.plan[5];
+    P.iters = e.plan[6];
+    smem = e.smem;
+    return e.found;
+}
+
+// Workspace of a call: per-channel partial sums of every slab (one for the
+// gradients of the on-chip form), and the gradient's two coefficients a group.
+size_t part_bytes(GnParams P, int vec, int32_t dtype, bool bwd, bool &chip) {
+    int64_t smem;
+    if ((chip = plan_chip(P, vec, dtype, bwd, smem))) {
+        if (!bwd) return 0;
+        P.slabs = 1;
+    } else {
+        split(P, vec);
+    }
+    return static_cast<size_t>(round_up(int64_t(P.N) * P.slabs * 2 * P.C * 4, 256));
+}
+size_t workspace_bytes(const GnParams &P, int vec, int32_t dtype, bool bwd) {
+    bool chip;
+    const size_t n = part_bytes(P, vec, dtype, bwd, chip);
+    return n + (bwd && !chip ? static_cast<size_t>(round_up(int64_t(P.N) * P.G * 8, 256)) : 0);
 }
 
 template <typename T, int VEC>
@@ -194,6 +230,7 @@ mqc_status launch_vec(GnParams &P, int vec, int32_t dtype, bool bwd, const Devic
 }
 
 mqc_status check_workspace(const char *name, const void *ws, size_t bytes, size_t need) {
+    if (need == 0) return MQC_OK;
     if (ws == nullptr || bytes < need)
         return fail(MQC_ERR_WORKSPACE, "%s: needs %zu workspace bytes, got %zu", name, need, ws ? bytes : size_t(0));
     if (!aligned16(ws)) return fail(MQC_ERR_ALIGNMENT, "%s: workspace not 16-byte aligned", name);
@@ -212,10 +249,6 @@ mqc_status run(const char *name, GnParams &P, int vec, int32_t dtype, bool bwd, 
     return launch_vec<__half>(P, vec, dtype, bwd, d, s);
 }
 
-size_t part_bytes(const mqc_t4 *d, int32_t dtype) {
-    return static_cast<size_t>(round_up(int64_t(d->d0) * most_slabs(d, dtype) * 2 * d->d1 * 4, 256));
-}
-
 void fill(GnParams &P, const mqc_t4 *d, int32_t groups) {
     P.N = d->d0;
     P.C = d->d1;
@@ -231,9 +264,25 @@ using namespace mqc;
 
 extern "C" {
 
-size_t mqc_group_norm_workspace_bytes(const mqc_t4 *d, int32_t dtype, int32_t groups) {
-    if (check_extents("group_norm_workspace_bytes", d, dtype, groups, MQC_ACT_NONE) != MQC_OK || d->d0 == 0) return 0;
-    return part_bytes(d, dtype) + static_cast<size_t>(round_up(int64_t(d->d0) * groups * 8, 256));
+size_t mqc_group_norm_fwd_workspace_bytes(const mqc_t4 *xd, const mqc_t4 *yd, int32_t dtype, int32_t groups) {
+    const char *name = "group_norm_fwd_workspace_bytes";
+    if (check_extents(name, xd, dtype, groups, MQC_ACT_NONE) != MQC_OK || yd == nullptr || xd->d0 == 0) return 0;
+    GnParams P{};
+    fill(P, xd, groups);
+    const mqc_t4 *all[2] = {xd, yd};
+    return workspace_bytes(P, vector_of(dtype, all, 2), dtype, false);
+}
+
+size_t mqc_group_norm_bwd_workspace_bytes(const mqc_t4 *gd, const mqc_t4 *xd, const mqc_t4 *gxd, int32_t dtype,
+                                          int32_t groups) {
+    const char *name = "group_norm_bwd_workspace_bytes";
+    if (check_extents(name, xd, dtype, groups, MQC_ACT_NONE) != MQC_OK || gd == nullptr || gxd == nullptr ||
+        xd->d0 == 0)
+        return 0;
+    GnParams P{};
+    fill(P, xd, groups);
+    const mqc_t4 *all[3] = {xd, gd, gxd};
+    return workspace_bytes(P, vector_of(dtype, all, 3), dtype, true);
 }
 
 mqc_status mqc_group_norm_fwd(const void *x, const mqc_t4 *xd, int32_t dtype, const float *gamma, const float *beta,
@@ -247,10 +296,12 @@ mqc_status mqc_group_norm_fwd(const void *x, const mqc_t4 *xd, int32_t dtype, co
     if ((st = check_tensor(name, "x", x, xd, xd)) != MQC_OK) return st;
     if ((st = check_tensor(name, "y", y, yd, xd)) != MQC_OK) return st;
     if (mean == nullptr || rstd == nullptr) return fail(MQC_ERR_INVALID, "%s: null statistics", name);
-    const size_t need = mqc_group_norm_workspace_bytes(xd, dtype, groups);
-    if ((st = check_workspace(name, workspace, workspace_bytes, need)) != MQC_OK) return st;
     GnParams P{};
     fill(P, xd, groups);
+    const mqc_t4 *all[2] = {xd, yd};
+    const int vec = vector_of(dtype, all, 2);
+    const size_t need = mqc::workspace_bytes(P, vec, dtype, false);
+    if ((st = check_workspace(name, workspace, workspace_bytes, need)) != MQC_OK) return st;
     P.x = tensor_of(x, xd);
     const GnTensor o = tensor_of(y, yd);
     P.out = y;
@@ -263,8 +314,7 @@ mqc_status mqc_group_norm_fwd(const void *x, const mqc_t4 *xd, int32_t dtype, co
     P.eps = eps;
     P.act = act;
     P.part = static_cast<float *>(workspace);
-    const mqc_t4 *all[2] = {xd, yd};
-    return run(name, P, vector_of(dtype, all, 2), dtype, false, static_cast<cudaStream_t>(stream));
+    return run(name, P, vec, dtype, false, static_cast<cudaStream_t>(stream));
 }
 
 mqc_status mqc_group_norm_bwd(const void *g, const mqc_t4 *gd, const void *x, const mqc_t4 *xd, int32_t dtype,
@@ -285,10 +335,12 @@ mqc_status mqc_group_norm_bwd(const void *g, const mqc_t4 *gd, const void *x, co
     if ((st = check_tensor(name, "g", g, gd, xd)) != MQC_OK) return st;
     if ((st = check_tensor(name, "gx", gx, gxd, xd)) != MQC_OK) return st;
     if (mean == nullptr || rstd == nullptr) return fail(MQC_ERR_INVALID, "%s: null statistics", name);
-    const size_t need = mqc_group_norm_workspace_bytes(xd, dtype, groups);
-    if ((st = check_workspace(name, workspace, workspace_bytes, need)) != MQC_OK) return st;
     GnParams P{};
     fill(P, xd, groups);
+    const mqc_t4 *all[3] = {xd, gd, gxd};
+    const int vec = vector_of(dtype, all, 3);
+    const size_t need = mqc::workspace_bytes(P, vec, dtype, true);
+    if ((st = check_workspace(name, workspace, workspace_bytes, need)) != MQC_OK) return st;
     P.x = tensor_of(x, xd);
     P.g = tensor_of(g, gd);
     const GnTensor o = tensor_of(gx, gxd);
@@ -303,9 +355,9 @@ mqc_status mqc_group_norm_bwd(const void *g, const mqc_t4 *gd, const void *x, co
     P.gbeta = gbeta;
     P.act = act;
     P.part = static_cast<float *>(workspace);
-    P.coef = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(xd, dtype));
-    const mqc_t4 *all[3] = {xd, gd, gxd};
-    return run(name, P, vector_of(dtype, all, 3), dtype, true, s);
+    bool chip;
+    P.coef = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(P, vec, dtype, true, chip));
+    return run(name, P, vec, dtype, true, s);
 }
 
 }  // extern "C"

@@ -387,7 +387,8 @@ typedef enum { MQC_F32 = 0, MQC_BF16 = 1, MQC_F16 = 2 } mqc_dtype;
  *   gamma, beta   fp32 [C]; NULL stands for ones / zeros.
  *   groups  divides C.      eps >= 0.     act  MQC_ACT_*, GELU included.
  *   mean, rstd    fp32 [N][groups], written (the backward pass reads them).
- *   workspace     at least mqc_group_norm_workspace_bytes() bytes of scratch.
+ *   workspace     at least mqc_group_norm_fwd_workspace_bytes() bytes of
+ *           scratch; may be NULL when that is 0.
  * N = 0 writes nothing and succeeds; C, H and W are at least 1.
  * Errors: MQC_ERR_INVALID, MQC_ERR_UNSUPPORTED, MQC_ERR_ALIGNMENT,
  * MQC_ERR_WORKSPACE, MQC_ERR_CUDA. */
@@ -406,14 +407,18 @@ MQC_API mqc_status mqc_group_norm_fwd(const void *x, const mqc_t4 *xd, int32_t d
  *   mean, rstd   as mqc_group_norm_fwd wrote them.
  *   ggamma, gbeta   fp32 [C], overwritten; either may be NULL.  N = 0 writes
  *           zeros.  The sums are taken in a fixed order.
+ *   workspace   at least mqc_group_norm_bwd_workspace_bytes() bytes.
  * Errors: as mqc_group_norm_fwd. */
 MQC_API mqc_status mqc_group_norm_bwd(const void *g, const mqc_t4 *gd, const void *x, const mqc_t4 *xd, int32_t dtype,
                               const float *gamma, const float *beta, const float *mean, const float *rstd,
                               int32_t groups, int32_t act, void *gx, const mqc_t4 *gxd, float *ggamma,
                               float *gbeta, void *workspace, size_t workspace_bytes, void *stream);
 
-/* Scratch of both directions for tensors of these extents. */
-MQC_API size_t mqc_group_norm_workspace_bytes(const mqc_t4 *xd, int32_t dtype, int32_t groups);
+/* Scratch of the two directions for tensors of these extents and strides (0:
+ * none is needed; an image's channels stay on chip between the passes). */
+MQC_API size_t mqc_group_norm_fwd_workspace_bytes(const mqc_t4 *xd, const mqc_t4 *yd, int32_t dtype, int32_t groups);
+MQC_API size_t mqc_group_norm_bwd_workspace_bytes(const mqc_t4 *gd, const mqc_t4 *xd, const mqc_t4 *gxd, int32_t dtype,
+                                          int32_t groups);
 
 /* One linear layer: M rows (tokens, pixels) of K features to N features.
  * Every matrix is row-major with its own row stride in elements (at least

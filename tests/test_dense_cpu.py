@@ -136,8 +136,13 @@ def test_group_norm_refusals(mqc):
     assert fwd(yd=d(s=nchw)) == -2
     assert fwd(d(s=(120, 1, 80, 8))) == -2           # a gap between rows of pixels
     assert fwd(d(s=(120, 1, 20, 4))) == -2           # overlapping pixels
-    need = mqc.mqc_group_norm_workspace_bytes(d(), 1, 4)
-    assert need > 0 and fwd(n=need - 1) == -6 and fwd(ws=None) == -6 and fwd(ws=ODD) == -5
+    assert mqc.mqc_group_norm_fwd_workspace_bytes(d(), d(), 1, 4) == 0      # on chip
+    wide = lambda n=2: d(n, 32, 400, 400)   # noqa: E731  (1.28 M elements a chunk of eight channels: beyond a cluster)
+    need = mqc.mqc_group_norm_fwd_workspace_bytes(wide(), wide(), 0, 4)
+    assert need > 0 and fwd(wide(), dtype=0, n=need - 1) == -6 and fwd(wide(), dtype=0, ws=None) == -6
+    assert fwd(wide(), dtype=0, ws=ODD) == -5
+    need = mqc.mqc_group_norm_bwd_workspace_bytes(d(), d(), d(), 1, 4)
+    assert need > 0
 
     def bwd(gd=None, g=P16, x=P16, gx=P16, mean=P16, rstd=P16, groups=4, a=0, ws=P16, n=1 << 20):
         return mqc.mqc_group_norm_bwd(g, gd or d(), x, d(), 1, None, None, mean, rstd, groups, a, gx, d(), P16, P16,

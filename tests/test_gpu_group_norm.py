@@ -249,7 +249,8 @@ def test_workspace_and_outputs_between_guard_bands(mqc):
         t = make(n, c, h, w, BF16)
         xd = mqc.T4(n, c, h, w, *t["x"].stride())
         sizes = dict(y=n * c * h * w * 2, mean=n * groups * 4, rstd=n * groups * 4, gg=c * 4, gb=c * 4,
-                     ws=mqc.mqc_group_norm_workspace_bytes(xd, mqc.BF16, groups))
+                     ws=max(mqc.mqc_group_norm_fwd_workspace_bytes(xd, xd, mqc.BF16, groups),
+                                mqc.mqc_group_norm_bwd_workspace_bytes(xd, xd, xd, mqc.BF16, groups), 1))
         bufs = {k: torch.full((v + 8192,), 0x5A, dtype=torch.uint8, device="cuda") for k, v in sizes.items()}
         at = {k: v.data_ptr() + 4096 for k, v in bufs.items()}
         p = lambda v: v.data_ptr()  # noqa: E731
