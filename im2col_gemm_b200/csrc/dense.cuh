@@ -83,68 +83,155 @@ struct Vec<float> {
     }
 };
 
-// Activations in fp32.  ReLU passes NaN on.  SiLU uses CUDA's fast exponential
-// and division (a relative error of a few 2^-23 where the value matters).
-// GELU takes the normal distribution from Abramowitz and Stegun 7.1.26
-// (Handbook of Mathematical Functions, 1964): erfc(x) = t (a1 + ... + a5 t^4)
-// exp(-x^2), t = 1 / (1 + p x), off by at most 1.5e-7: one reciprocal and one
-// exponential without a branch (erff has two ranges, and lanes of both in a
-// warp pay for both).
+// Two fp32 values in one register pair: sm_100 adds, multiplies and fuses both
+// with one instruction, each rounded as the plain operation is.
+__device__ __forceinline__ uint64_t bits2(float2 v) {
+    uint64_t b;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(v.x), "f"(v.y));
+    return b;
+}
+__device__ __forceinline__ float2 float2_of(uint64_t b) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(b));
+    return v;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return float2_of(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return float2_of(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return float2_of(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// 2^x and 1/x, subnormals as zero (a relative error of about 2^-22).
+__device__ __forceinline__ float2 exp2_2(float2 v) {
+    float2 r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ float2 rcp_2(float2 v) {
+    float2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+    return r;
+}
+
+// Activations in fp32, two elements at a time.  ReLU passes NaN on.  GELU
+// takes the normal distribution from Abramowitz and Stegun 7.1.26 (Handbook of
+// Mathematical Functions, 1964): erfc(x) = t (a1 + ... + a5 t^4) exp(-x^2), t
+// = 1 / (1 + p x), off by at most 1.5e-7: one reciprocal and one exponential
+// without a branch (erff has two ranges, and lanes of both in a warp pay for
+// both).
 struct Relu {
-    __device__ static __forceinline__ float value(float z) { return z < 0.f ? 0.f : z; }
-    __device__ static __forceinline__ float slope(float z) { return z > 0.f ? 1.f : 0.f; }
+    __device__ static __forceinline__ float2 value(float2 z) {
+        return make_float2(z.x < 0.f ? 0.f : z.x, z.y < 0.f ? 0.f : z.y);
+    }
+    __device__ static __forceinline__ float2 slope(float2 z) {
+        return make_float2(z.x > 0.f ? 1.f : 0.f, z.y > 0.f ? 1.f : 0.f);
+    }
 };
 struct Silu {
-    __device__ static __forceinline__ float value(float z) { return __fdividef(z, 1.f + __expf(-z)); }
-    // q (1 + z (1 - q)), q = sigmoid(z)
-    __device__ static __forceinline__ float slope(float z) {
-        const float q = __fdividef(1.f, 1.f + __expf(-z));
-        return q * (1.f + z * (1.f - q));
+    __device__ static __forceinline__ float2 sigmoid(float2 z) {
+        return rcp_2(add2(exp2_2(mul2(z, both(-1.4426950408889634f))), both(1.f)));
     }
+    __device__ static __forceinline__ float2 value(float2 z) { return mul2(z, sigmoid(z)); }
+    // q + q z (1 - q), q = sigmoid(z)
+    __device__ static __forceinline__ float2 slope_of(float2 z, float2 q) {
+        const float2 m = make_float2(-q.x, -q.y);
+        return fma2(q, fma2(m, z, z), q);
+    }
+    __device__ static __forceinline__ float2 slope(float2 z) { return slope_of(z, sigmoid(z)); }
+};
+// The same with one reciprocal for two elements, of the product of their
+// denominators, where exponentials and reciprocals (an eighth of the rate of
+// other arithmetic) bound a pass; an element's last bits then depend on its
+// neighbour.  Denominators stop at 2^62, so that their product is finite;
+// below z = -43, where sigmoid is under 2^-62, it is given as 0.
+struct SiluPair {
+    __device__ static __forceinline__ float2 sigmoid(float2 z) {
+        float2 t = mul2(z, both(-1.4426950408889634f));
+        t = make_float2(fminf(t.x, 62.f), fminf(t.y, 62.f));
+        const float2 d = add2(exp2_2(t), both(1.f));
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
+        const float2 q = mul2(make_float2(d.y, d.x), both(r));
+        return make_float2(t.x < 62.f ? q.x : z.x * 0.f, t.y < 62.f ? q.y : z.y * 0.f);
+    }
+    __device__ static __forceinline__ float2 value(float2 z) { return mul2(z, sigmoid(z)); }
+    __device__ static __forceinline__ float2 slope(float2 z) { return Silu::slope_of(z, sigmoid(z)); }
 };
 struct Gelu {
     // Phi(z), with e = exp(-z^2 / 2)
-    __device__ static __forceinline__ float phi(float z, float e) {
-        const float t = __fdividef(1.f, fmaf(0.3275911f * 0.70710678118654752f, fabsf(z), 1.f));
-        float c = fmaf(1.061405429f, t, -1.453152027f);
-        c = fmaf(c, t, 1.421413741f);
-        c = fmaf(c, t, -0.284496736f);
-        c = fmaf(c, t, 0.254829592f);
-        c = 0.5f * c * t * e;
-        return z > 0.f ? 1.f - c : c;
+    __device__ static __forceinline__ float2 phi(float2 z, float2 e) {
+        const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
+        const float2 t = rcp_2(fma2(a, both(0.3275911f * 0.70710678118654752f), both(1.f)));
+        float2 c = fma2(both(0.5f * 1.061405429f), t, both(0.5f * -1.453152027f));
+        c = fma2(c, t, both(0.5f * 1.421413741f));
+        c = fma2(c, t, both(0.5f * -0.284496736f));
+        c = fma2(c, t, both(0.5f * 0.254829592f));
+        c = mul2(mul2(c, t), e);
+        return make_float2(z.x > 0.f ? 1.f - c.x : c.x, z.y > 0.f ? 1.f - c.y : c.y);
     }
-    __device__ static __forceinline__ float value(float z) { return z * phi(z, __expf(-0.5f * z * z)); }
-    __device__ static __forceinline__ float slope(float z) {
-        const float e = __expf(-0.5f * z * z);
-        return fmaf(z * 0.39894228040143268f, e, phi(z, e));
+    __device__ static __forceinline__ float2 bell(float2 z) {
+        return exp2_2(mul2(mul2(z, both(-0.5f * 1.4426950408889634f)), z));
+    }
+    __device__ static __forceinline__ float2 value(float2 z) { return mul2(z, phi(z, bell(z))); }
+    __device__ static __forceinline__ float2 slope(float2 z) {
+        const float2 e = bell(z);
+        return fma2(mul2(z, both(0.39894228040143268f)), e, phi(z, e));
     }
 };
 
-// v = act(v); s = act'(z).  One branch for all N elements.
-template <int N>
-__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
-    if (act == MQC_ACT_RELU) {
+// v = act(v); s = act'(z).  One branch for all N elements.  PAIR: SiLU with
+// shared reciprocals.
+template <bool FIRST, typename A, typename B>
+struct Either { using type = A; };
+template <typename A, typename B>
+struct Either<false, A, B> { using type = B; };
+template <typename A, int N>
+__device__ __forceinline__ void map_values(float (&v)[N]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = Relu::value(v[i]);
-    } else if (act == MQC_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = Silu::value(v[i]);
-    } else if (act == MQC_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = Gelu::value(v[i]);
+    for (int i = 0; i + 1 < N; i += 2) {
+        const float2 r = A::value(make_float2(v[i], v[i + 1]));
+        v[i] = r.x;
+        v[i + 1] = r.y;
     }
+    if (N % 2) v[N - 1] = A::value(both(v[N - 1])).x;
 }
-template <int N>
+template <typename A, int N>
+__device__ __forceinline__ void map_slopes(const float (&z)[N], float (&s)[N]) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+        const float2 r = A::slope(make_float2(z[i], z[i + 1]));
+        s[i] = r.x;
+        s[i + 1] = r.y;
+    }
+    if (N % 2) s[N - 1] = A::slope(both(z[N - 1])).x;
+}
+template <bool PAIR = false, int N>
+__device__ __forceinline__ void act_values(int act, float (&v)[N]) {
+    if (act == MQC_ACT_RELU) map_values<Relu>(v);
+    else if (act == MQC_ACT_SILU) map_values<typename Either<PAIR, SiluPair, Silu>::type>(v);
+    else if (act == MQC_ACT_GELU) map_values<Gelu>(v);
+}
+template <bool PAIR = false, int N>
 __device__ __forceinline__ void act_slopes(int act, const float (&z)[N], float (&s)[N]) {
     if (act == MQC_ACT_RELU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = Relu::slope(z[i]);
+        map_slopes<Relu>(z, s);
     } else if (act == MQC_ACT_SILU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = Silu::slope(z[i]);
+        map_slopes<typename Either<PAIR, SiluPair, Silu>::type>(z, s);
     } else if (act == MQC_ACT_GELU) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) s[i] = Gelu::slope(z[i]);
+        map_slopes<Gelu>(z, s);
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] = 1.f;
@@ -154,6 +241,39 @@ __device__ __forceinline__ float act_value(int act, float z) {
     float v[1] = {z};
     act_values(act, v);
     return v[0];
+}
+
+// Elementwise arithmetic on N fp32 values, two at a time where N is even.
+template <int N>
+__device__ __forceinline__ void add_to(float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+        const float2 r = add2(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+        a[i] = r.x;
+        a[i + 1] = r.y;
+    }
+    if (N % 2) a[N - 1] += b[N - 1];
+}
+template <int N>
+__device__ __forceinline__ void mul_to(float (&a)[N], const float (&b)[N]) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+        const float2 r = mul2(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+        a[i] = r.x;
+        a[i + 1] = r.y;
+    }
+    if (N % 2) a[N - 1] *= b[N - 1];
+}
+// r = a b + c
+template <int N>
+__device__ __forceinline__ void fma_to(float (&r)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+#pragma unroll
+    for (int i = 0; i + 1 < N; i += 2) {
+        const float2 v = fma2(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]), make_float2(c[i], c[i + 1]));
+        r[i] = v.x;
+        r[i + 1] = v.y;
+    }
+    if (N % 2) r[N - 1] = fmaf(a[N - 1], b[N - 1], c[N - 1]);
 }
 
 }  // namespace mqc

@@ -37,50 +37,47 @@ mqc_status check_extents(const char *name, const mqc_t4 *d, int32_t dtype, int32
     return MQC_OK;
 }
 
-// Elements of one access: the most, up to 16 bytes, that divides the channels
-// and every stride.
-int vector_of(int32_t dtype, const mqc_t4 *const *d, int count) {
+// Elements of one access: the most, up to `most` and 16 bytes, that divides the
+// channels and every stride.  (Backward four: eight channels' constants and
+// sums take 128 registers, and the fewer warps cost more than the wider loads
+// gain.)
+int vector_of(int32_t dtype, const mqc_t4 *const *d, int count, int most) {
     int64_t bits = d[0]->d1;
     for (int i = 0; i < count; ++i) {
         if (d[i]->d2 * int64_t(d[i]->d3) > 1) bits |= d[i]->d3 > 1 ? d[i]->s3 : d[i]->s2;
         if (d[i]->d0 > 1) bits |= d[i]->s0;
     }
-    int v = 16 / dtype_bytes(dtype);
+    int v = std::min(most, 16 / dtype_bytes(dtype));
     while (bits % v != 0) v /= 2;
     return v;
-}
-
-// The split of a tensor into blocks: channel vectors along tx, pixels along
-// ty, and pixel slabs so that there are about 16 blocks an SM (148 of them)
-// while a thread still has at least four pixels.
-void split(GnParams &P, int vec) {
-    const int64_t cv = P.C / vec;
-    P.tx = static_cast<int32_t>(std::min<int64_t>(cv, kGnThreads));
-    P.ty = kGnThreads / P.tx;
-    P.col_blocks = static_cast<int32_t>(ceil_div(cv, P.tx));
-    const int64_t want = std::max<int64_t>(1, 148 * 16 / std::max<int64_t>(1, int64_t(P.N) * P.col_blocks));
-    const int64_t most = ceil_div(P.HW, int64_t(P.ty) * 4);
-    P.slab = static_cast<int32_t>(ceil_div(P.HW, std::min(want, most)));
-    P.slabs = static_cast<int32_t>(ceil_div(P.HW, P.slab));
 }
 
 GnTensor tensor_of(const void *p, const mqc_t4 *d) {
     return GnTensor{p, d->d0 > 1 ? d->s0 : 0, d->d3 > 1 ? d->s3 : d->s2};
 }
 
-// Shared memory of the on-chip form besides the slots: row sums, 256 partial
-// sums, two channel sums, four group sums, and the slots' alignment.
-int64_t chip_extra(int tx, int ty, int vec, int gpc) {
-    return 16 + 4 * (int64_t(tx) * ty * vec + kGnThreads + 2 * int64_t(tx) * vec + 4 * int64_t(gpc));
-}
-constexpr int64_t kChipSmem = 200 * 1024;
+// Sums that a thread leaves for the groups of its vector: one when the vector
+// lies in one group, one a group when groups tile the vector, else one a
+// channel.
+int sums_left(int D, int vec) { return D % vec == 0 ? 1 : (vec % D == 0 ? vec / D : vec); }
 
-// The on-chip form of a tensor, if a cluster of at most eight CTAs holds one
-// image's chunk of channels: the chunk (whole groups, whole vectors) and the
-// number of CTAs with the least estimated time, in ns: the busiest SM's bytes
-// at its share of the memory bandwidth (43 bytes/ns; rows below 32 bytes waste
-// sectors), and for each round of resident CTAs the latency of loads and
-// barriers, half hidden when several CTAs share an SM.
+// Shared memory of the on-chip form besides the slots (and their alignment):
+// row sums, group sums; backward also a partial and a channel sum, all twice.
+int64_t chip_extra(int64_t tx, int64_t ty, int vec, int D, int64_t gpc, int threads, bool bwd) {
+    return 16 + 4 * (bwd ? 2 * tx * ty * vec + 2 * threads + 2 * tx * vec + 4 * gpc
+                         : tx * ty * sums_left(D, vec) + 4 * gpc);
+}
+constexpr int kChipSmem = 200 * 1024;
+
+// The on-chip form of a tensor, if a cluster of at most 16 CTAs holds one
+// image's chunk of channels: the chunk (whole groups, whole vectors), threads
+// and CTAs of the least estimated time.  In ns, for one round of the CTAs that
+// an SM holds at once: their loads at the SM's share of the memory bandwidth
+// (43 bytes/ns; rows below 64 bytes waste half of it), then the larger of
+// their stores and their arithmetic (about 14 warp instructions an element
+// forward, 26 backward, and 300 a thread for constants and sums, at 0.16 a
+// cycle for each warp of a scheduler, up to 0.75), and the latency of loads
+// and barriers.
 bool search_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
     const int size = dtype_bytes(dtype);
     if (vec * size < 4) return false;
@@ -89,29 +86,37 @@ bool search_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
         if (P.G % gpc != 0 || (int64_t(gpc) * P.D) % vec != 0) continue;
         const int64_t tx = int64_t(gpc) * P.D / vec;
         if (tx > kGnThreads) break;
-        const int ty = static_cast<int>(kGnThreads / tx);
         const int64_t row = int64_t(gpc) * P.D * size;
-        for (int splits = 1; splits <= 8; splits *= 2) {
-            const int64_t slab = ceil_div(P.HW, splits), iters = ceil_div(slab, ty);
-            const int64_t need = iters * tx * ty * vec * size * (bwd ? 2 : 1) +
-                                 chip_extra(static_cast<int>(tx), ty, vec, gpc);
-            if (need > kChipSmem || (splits > 1 && slab * (splits - 1) >= P.HW)) continue;
-            const int64_t ctas = int64_t(P.N) * (P.G / gpc) * splits;
-            const int64_t resident = std::min<int64_t>(4, (228 * 1024) / (need + 1024));
-            const double waste = row < 32 ? 32.0 / row : (row < 64 ? 1.1 : 1.0);
-            const double moved = double(slab) * row * (bwd ? 3 : 2) * waste;
-            const double ns = ceil_div(ctas, 148) * moved / 43.0 +
-                              ceil_div(ctas, 148 * resident) * (resident > 1 ? 1500.0 : 3000.0) + (splits > 1 ? 500.0 : 0.0);
-            if (ns < best) {
-                best = ns;
-                P.gpc = gpc;
-                P.chunks = P.G / gpc;
-                P.tx = static_cast<int32_t>(tx);
-                P.ty = ty;
-                P.splits = splits;
-                P.slab = static_cast<int32_t>(slab);
-                P.iters = static_cast<int32_t>(iters);
-                smem = need;
+        const double waste = row < 64 ? std::min(4.0, 96.0 / row) / 1.5 : 1.0;
+        for (int threads = kGnThreads; threads >= 128 && threads >= tx; threads /= 2) {
+            const int ty = static_cast<int>(threads / tx);
+            for (int splits = 1; splits <= 16; splits *= 2) {
+                const int64_t slab = ceil_div(P.HW, splits), iters = ceil_div(slab, ty);
+                const int64_t need = iters * tx * ty * vec * size * (bwd ? 2 : 1) +
+                                     chip_extra(tx, ty, vec, P.D, gpc, threads, bwd);
+                if (need > kChipSmem || slab * (splits - 1) >= P.HW) continue;
+                const int64_t ctas = int64_t(P.N) * (P.G / gpc) * splits;
+                const int64_t regs = bwd && vec == 8 ? 104 : 64;
+                const int64_t resident = std::max<int64_t>(
+                    1, std::min({ceil_div(ctas, 148), 65536 / (threads * regs), (228 * 1024) / (need + 1024)}));
+                const double bytes = resident * double(slab) * row * waste / 43.0;
+                const double warps = resident * threads / 128.0;
+                const double issued = warps * (300.0 + iters * vec * (bwd ? 26.0 : 14.0)) /
+                                      (1.9 * std::min(0.75, 0.16 * warps));
+                const double round = bytes * (bwd ? 2 : 1) + std::max(bytes, issued) + (splits > 1 ? 3000.0 : 1800.0);
+                const double ns = std::max(1.0, double(ctas) / (148 * resident)) * round;
+                if (ns < best) {
+                    best = ns;
+                    P.gpc = gpc;
+                    P.chunks = P.G / gpc;
+                    P.tx = static_cast<int32_t>(tx);
+                    P.ty = ty;
+                    P.threads = threads;
+                    P.splits = splits;
+                    P.slab = static_cast<int32_t>(slab);
+                    P.iters = static_cast<int32_t>(iters);
+                    smem = need;
+                }
             }
         }
     }
@@ -121,7 +126,7 @@ bool search_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
 // The same, remembered by sizes (the search takes some microseconds).
 bool plan_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
     struct Entry {
-        int32_t key[7], plan[7];
+        int32_t key[7], plan[8];
         int64_t smem;
         bool used, found;
     };
@@ -133,7 +138,7 @@ bool plan_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
     if (!e.used || memcmp(e.key, key, sizeof key) != 0) {
         e.found = search_chip(P, vec, dtype, bwd, smem);
         memcpy(e.key, key, sizeof key);
-        const int32_t plan[7] = {P.gpc, P.chunks, P.tx, P.ty, P.splits, P.slab, P.iters};
+        const int32_t plan[8] = {P.gpc, P.chunks, P.tx, P.ty, P.splits, P.slab, P.iters, P.threads};
         memcpy(e.plan, plan, sizeof plan);
         e.smem = smem;
         e.used = true;
@@ -146,46 +151,98 @@ bool plan_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
     P.splits = e.plan[4];
     P.slab = e.plan[5];
     P.iters = e.plan[6];
+    P.threads = e.plan[7];
     smem = e.smem;
     return e.found;
 }
 
-// Workspace of a call: per-channel partial sums of every slab (one for the
-// gradients of the on-chip form), and the gradient's two coefficients a group.
-size_t part_bytes(GnParams P, int vec, int32_t dtype, bool bwd, bool &chip) {
-    int64_t smem;
-    if ((chip = plan_chip(P, vec, dtype, bwd, smem))) {
-        if (!bwd) return 0;
-        P.slabs = 1;
-    } else {
-        split(P, vec);
+// The two-pass form: chunks of whole groups and whole vectors, about 512 bytes
+// wide, or pieces of a group wider than a block; slabs of pixels so that there
+// are about eight blocks of 256 threads for each of 148 SMs while a thread
+// still has eight pixels.  Returns the elements of a vector.
+int plan_passes(GnParams &P, int vec, int32_t dtype) {
+    int unit;   // groups that are whole vectors
+    for (;; vec /= 2) {
+        unit = 1;
+        while ((int64_t(unit) * P.D) % vec != 0) ++unit;
+        if (int64_t(unit) * P.D / vec <= kPassThreads || P.D % vec == 0) break;
     }
-    return static_cast<size_t>(round_up(int64_t(P.N) * P.slabs * 2 * P.C * 4, 256));
-}
-size_t workspace_bytes(const GnParams &P, int vec, int32_t dtype, bool bwd) {
-    bool chip;
-    const size_t n = part_bytes(P, vec, dtype, bwd, chip);
-    return n + (bwd && !chip ? static_cast<size_t>(round_up(int64_t(P.N) * P.G * 8, 256)) : 0);
+    P.splits = 0;
+    if (int64_t(unit) * P.D / vec > kPassThreads) {   // unit = 1
+        P.gpc = 1;
+        P.width = kPassThreads * vec;
+        P.pieces = static_cast<int32_t>(ceil_div(P.D, P.width));
+        P.chunks = P.G * P.pieces;
+    } else {
+        P.gpc = unit;
+        for (int g = unit; g <= P.G; g += unit)
+            if (P.G % g == 0 && int64_t(g) * P.D * dtype_bytes(dtype) <= 512) P.gpc = g;
+        P.pieces = 1;
+        P.width = P.gpc * P.D;
+        P.chunks = P.G / P.gpc;
+    }
+    P.tx = P.width / vec;
+    P.threads = kPassThreads;
+    P.ty = P.threads / P.tx;
+    const int64_t want = std::max<int64_t>(1, 148 * 8 / std::max<int64_t>(1, int64_t(P.N) * P.chunks));
+    const int64_t most = ceil_div(P.HW, int64_t(P.ty) * 8);
+    P.slab = static_cast<int32_t>(ceil_div(P.HW, std::min(want, most)));
+    P.slabs = static_cast<int32_t>(ceil_div(P.HW, P.slab));
+    return vec;
 }
 
-template <typename T, int VEC>
-mqc_status launch(GnParams &P, int32_t dtype, bool bwd, const DeviceLimits &d, cudaStream_t s) {
-    const int64_t cb = P.ggamma || P.gbeta ? ceil_div(P.C, 32) : 0;
-    int64_t smem = 0;
+// The plan of a call and its workspace: backward, the channels' partial sums of
+// every slab (one an image on chip); in two passes, the groups' too.
+struct GnPlan {
+    int vec;
+    bool chip;
+    int64_t smem, part, gpart;
+    int64_t bytes() const { return part + gpart; }
+};
+GnPlan make_plan(GnParams &P, int vec, int32_t dtype, bool bwd) {
+    GnPlan p{vec, false, 0, 0, 0};
+    p.chip = plan_chip(P, vec, dtype, bwd, p.smem);
+    if (p.chip) {
+        P.slabs = 1;
+        P.pieces = 1;
+        P.width = P.tx * vec;
+    } else {
+        p.vec = plan_passes(P, vec, dtype);
+        p.gpart = round_up(int64_t(P.N) * P.slabs * P.chunks * P.gpc * 8, 256);
+    }
+    if (bwd) p.part = round_up(int64_t(P.N) * P.slabs * 2 * P.C * 4, 256);
+    const int cb = P.tx * p.vec;
+    const bool uni = P.D % p.vec == 0;
+    P.seg = bwd ? std::max(1, P.threads / cb) : sums_left(P.D, p.vec);
+    P.fd_tx = make_fastdiv(P.tx);
+    P.fd_ty = make_fastdiv(P.ty);
+    P.fd_chunks = make_fastdiv(P.chunks);
+    P.fd_slabs = make_fastdiv(P.slabs);
+    P.fd_cb = make_fastdiv(cb);
+    P.fd_entries = make_fastdiv(uni ? (P.pieces > 1 ? P.tx : P.D / p.vec) : (P.seg == p.vec ? P.D : 1));
+    return p;
+}
+
+template <typename T, int VEC, bool UNI>
+mqc_status launch(GnParams &P, const GnPlan &plan, bool bwd, const DeviceLimits &d, cudaStream_t s) {
+    const int channel_blocks = bwd && (P.ggamma || P.gbeta) ? static_cast<int>(ceil_div(P.C, 32)) : 0;
     if constexpr (VEC * sizeof(T) >= 4)
-        if (plan_chip(P, VEC, dtype, bwd, smem)) {
-            void (*kernel)(GnParams) = bwd ? gn_chip_bwd_kernel<T, VEC> : gn_chip_fwd_kernel<T, VEC>;
+        if (plan.chip) {
+            void (*kernel)(GnParams) = bwd ? gn_chip_bwd_kernel<T, VEC, UNI> : gn_chip_fwd_kernel<T, VEC, UNI>;
             static std::atomic<bool> allowed[2][64];
             if (!allowed[bwd][d.device].load(std::memory_order_acquire)) {
                 cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kChipSmem);
+                if (e == cudaSuccess)
+                    e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
+                                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
                 if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(group norm)");
                 allowed[bwd][d.device].store(true, std::memory_order_release);
             }
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(static_cast<unsigned>(int64_t(P.N) * P.chunks * P.splits));
-            cfg.blockDim = dim3(kGnThreads);
-            cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+            cfg.blockDim = dim3(P.threads);
+            cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);
             cfg.stream = s;
             cudaLaunchAttribute at[1];
             at[0].id = cudaLaunchAttributeClusterDimension;
@@ -196,37 +253,37 @@ mqc_status launch(GnParams &P, int32_t dtype, bool bwd, const DeviceLimits &d, c
             cfg.numAttrs = 1;
             cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
             if (e != cudaSuccess) return cuda_fail(e, "group norm launch");
-            if (bwd && cb > 0) {
-                P.slabs = 1;
-                gn_bwd_finish_kernel<<<static_cast<unsigned>(cb), 128, 0, s>>>(P, 0);
+            if (channel_blocks > 0) {
+                gn_channels_kernel<<<channel_blocks, kGnThreads, 0, s>>>(P, P.N);
                 e = cudaGetLastError();
                 if (e != cudaSuccess) return cuda_fail(e, "group norm launch");
             }
             return MQC_OK;
         }
-    split(P, VEC);
-    const unsigned grid = static_cast<unsigned>(int64_t(P.N) * P.slabs * P.col_blocks);
-    const unsigned gb = static_cast<unsigned>(ceil_div(int64_t(P.N) * P.G, 4));
+    const unsigned grid = static_cast<unsigned>(int64_t(P.N) * P.slabs * P.chunks);
+    const size_t nt = size_t(P.tx) * P.ty, groups = 2 * size_t(P.gpc) * 4;
     if (bwd) {
-        gn_bwd_sums_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
-        gn_bwd_finish_kernel<<<gb + static_cast<unsigned>(cb), 128, 0, s>>>(P, static_cast<int32_t>(gb));
-        gn_bwd_apply_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
+        P.channel_blocks = channel_blocks;
+        const size_t sums = 4 * (2 * nt * VEC + 2 * P.threads + 2 * size_t(P.tx) * VEC);
+        const size_t join = P.threads / 32 * 2 * 32 * 8;
+        gn_bwd_sums_kernel<T, VEC, UNI><<<grid, P.threads, sums, s>>>(P);
+        gn_bwd_apply_kernel<T, VEC, UNI><<<grid + channel_blocks, P.threads, std::max(groups, join), s>>>(P);
     } else {
-        gn_stats_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
-        gn_finish_kernel<<<gb, 128, 0, s>>>(P);
-        gn_apply_kernel<T, VEC><<<grid, kGnThreads, 0, s>>>(P);
+        gn_stats_kernel<T, VEC, UNI><<<grid, P.threads, 4 * nt * (UNI ? 1 : P.seg) + groups, s>>>(P);
+        gn_apply_kernel<T, VEC, UNI><<<grid, P.threads, groups, s>>>(P);
     }
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "group norm launch");
 }
 
 template <typename T>
-mqc_status launch_vec(GnParams &P, int vec, int32_t dtype, bool bwd, const DeviceLimits &d, cudaStream_t s) {
+mqc_status launch_vec(GnParams &P, const GnPlan &plan, bool bwd, const DeviceLimits &d, cudaStream_t s) {
+    const bool uni = P.D % plan.vec == 0;   // always, with one channel a vector
     if constexpr (sizeof(T) == 2)
-        if (vec == 8) return launch<T, 8>(P, dtype, bwd, d, s);
-    if (vec == 4) return launch<T, 4>(P, dtype, bwd, d, s);
-    if (vec == 2) return launch<T, 2>(P, dtype, bwd, d, s);
-    return launch<T, 1>(P, dtype, bwd, d, s);
+        if (plan.vec == 8) return uni ? launch<T, 8, true>(P, plan, bwd, d, s) : launch<T, 8, false>(P, plan, bwd, d, s);
+    if (plan.vec == 4) return uni ? launch<T, 4, true>(P, plan, bwd, d, s) : launch<T, 4, false>(P, plan, bwd, d, s);
+    if (plan.vec == 2) return uni ? launch<T, 2, true>(P, plan, bwd, d, s) : launch<T, 2, false>(P, plan, bwd, d, s);
+    return launch<T, 1, true>(P, plan, bwd, d, s);
 }
 
 mqc_status check_workspace(const char *name, const void *ws, size_t bytes, size_t need) {
@@ -237,16 +294,16 @@ mqc_status check_workspace(const char *name, const void *ws, size_t bytes, size_
     return MQC_OK;
 }
 
-mqc_status run(const char *name, GnParams &P, int vec, int32_t dtype, bool bwd, cudaStream_t s) {
-    // every grid below has at most this many blocks
-    if (int64_t(P.N) * P.G * 8 > (int64_t(1) << 31) - 1 || int64_t(P.N) * P.C > (int64_t(1) << 31) - 1)
+mqc_status run(const char *name, GnParams &P, const GnPlan &plan, int32_t dtype, bool bwd, cudaStream_t s) {
+    // every grid above has at most this many blocks
+    if (int64_t(P.N) * P.G * 16 > (int64_t(1) << 31) - 1 || int64_t(P.N) * P.slabs * P.chunks > (int64_t(1) << 30))
         return fail(MQC_ERR_INVALID, "%s: tensor too large", name);
     DeviceLimits d;
     mqc_status st = device_limits(&d);
     if (st != MQC_OK) return st;
-    if (dtype == MQC_F32) return launch_vec<float>(P, vec, dtype, bwd, d, s);
-    if (dtype == MQC_BF16) return launch_vec<__nv_bfloat16>(P, vec, dtype, bwd, d, s);
-    return launch_vec<__half>(P, vec, dtype, bwd, d, s);
+    if (dtype == MQC_F32) return launch_vec<float>(P, plan, bwd, d, s);
+    if (dtype == MQC_BF16) return launch_vec<__nv_bfloat16>(P, plan, bwd, d, s);
+    return launch_vec<__half>(P, plan, bwd, d, s);
 }
 
 void fill(GnParams &P, const mqc_t4 *d, int32_t groups) {
@@ -270,7 +327,7 @@ size_t mqc_group_norm_fwd_workspace_bytes(const mqc_t4 *xd, const mqc_t4 *yd, in
     GnParams P{};
     fill(P, xd, groups);
     const mqc_t4 *all[2] = {xd, yd};
-    return workspace_bytes(P, vector_of(dtype, all, 2), dtype, false);
+    return static_cast<size_t>(make_plan(P, vector_of(dtype, all, 2, 8), dtype, false).bytes());
 }
 
 size_t mqc_group_norm_bwd_workspace_bytes(const mqc_t4 *gd, const mqc_t4 *xd, const mqc_t4 *gxd, int32_t dtype,
@@ -282,7 +339,7 @@ size_t mqc_group_norm_bwd_workspace_bytes(const mqc_t4 *gd, const mqc_t4 *xd, co
     GnParams P{};
     fill(P, xd, groups);
     const mqc_t4 *all[3] = {xd, gd, gxd};
-    return workspace_bytes(P, vector_of(dtype, all, 3), dtype, true);
+    return static_cast<size_t>(make_plan(P, vector_of(dtype, all, 3, 4), dtype, true).bytes());
 }
 
 mqc_status mqc_group_norm_fwd(const void *x, const mqc_t4 *xd, int32_t dtype, const float *gamma, const float *beta,
@@ -299,9 +356,8 @@ mqc_status mqc_group_norm_fwd(const void *x, const mqc_t4 *xd, int32_t dtype, co
     GnParams P{};
     fill(P, xd, groups);
     const mqc_t4 *all[2] = {xd, yd};
-    const int vec = vector_of(dtype, all, 2);
-    const size_t need = mqc::workspace_bytes(P, vec, dtype, false);
-    if ((st = check_workspace(name, workspace, workspace_bytes, need)) != MQC_OK) return st;
+    const GnPlan plan = make_plan(P, vector_of(dtype, all, 2, 8), dtype, false);
+    if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes())) != MQC_OK) return st;
     P.x = tensor_of(x, xd);
     const GnTensor o = tensor_of(y, yd);
     P.out = y;
@@ -313,8 +369,8 @@ mqc_status mqc_group_norm_fwd(const void *x, const mqc_t4 *xd, int32_t dtype, co
     P.rstd = rstd;
     P.eps = eps;
     P.act = act;
-    P.part = static_cast<float *>(workspace);
-    return run(name, P, vec, dtype, false, static_cast<cudaStream_t>(stream));
+    P.gpart = static_cast<float *>(workspace);
+    return run(name, P, plan, dtype, false, static_cast<cudaStream_t>(stream));
 }
 
 mqc_status mqc_group_norm_bwd(const void *g, const mqc_t4 *gd, const void *x, const mqc_t4 *xd, int32_t dtype,
@@ -338,9 +394,8 @@ mqc_status mqc_group_norm_bwd(const void *g, const mqc_t4 *gd, const void *x, co
     GnParams P{};
     fill(P, xd, groups);
     const mqc_t4 *all[3] = {xd, gd, gxd};
-    const int vec = vector_of(dtype, all, 3);
-    const size_t need = mqc::workspace_bytes(P, vec, dtype, true);
-    if ((st = check_workspace(name, workspace, workspace_bytes, need)) != MQC_OK) return st;
+    const GnPlan plan = make_plan(P, vector_of(dtype, all, 3, 4), dtype, true);
+    if ((st = check_workspace(name, workspace, workspace_bytes, plan.bytes())) != MQC_OK) return st;
     P.x = tensor_of(x, xd);
     P.g = tensor_of(g, gd);
     const GnTensor o = tensor_of(gx, gxd);
@@ -355,9 +410,8 @@ mqc_status mqc_group_norm_bwd(const void *g, const mqc_t4 *gd, const void *x, co
     P.gbeta = gbeta;
     P.act = act;
     P.part = static_cast<float *>(workspace);
-    bool chip;
-    P.coef = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + part_bytes(P, vec, dtype, true, chip));
-    return run(name, P, vec, dtype, true, s);
+    P.gpart = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + plan.part);
+    return run(name, P, plan, dtype, true, s);
 }
 
 }  // extern "C"

@@ -19,18 +19,49 @@ struct Pack {
     using Raw = typename RawOf<VEC * sizeof(T)>::type;
     __device__ static __forceinline__ Raw load(const T *p) { return *reinterpret_cast<const Raw *>(p); }
     __device__ static __forceinline__ void widen(const Raw &r, float (&v)[VEC]) {
-        const T *e = reinterpret_cast<const T *>(&r);
+        if constexpr (sizeof(T) == 2 && VEC >= 2) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) v[q] = to_f32(e[q]);
+            for (int q = 0; q < VEC / 2; ++q) {
+                const float2 f = unpack2<T>(w[q]);
+                v[2 * q] = f.x;
+                v[2 * q + 1] = f.y;
+            }
+        } else {
+            const T *e = reinterpret_cast<const T *>(&r);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) v[q] = to_f32(e[q]);
+        }
     }
     __device__ static __forceinline__ void store(T *p, const float (&v)[VEC]) {
         Raw r;
-        T *e = reinterpret_cast<T *>(&r);
+        if constexpr (sizeof(T) == 2 && VEC >= 2) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(&r);
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) e[q] = from_f32<T>(v[q]);
+            for (int q = 0; q < VEC / 2; ++q) w[q] = pack2<T>(v[2 * q], v[2 * q + 1]);
+        } else {
+            T *e = reinterpret_cast<T *>(&r);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) e[q] = from_f32<T>(v[q]);
+        }
         *reinterpret_cast<Raw *>(p) = r;
     }
 };
+
+// The group of each of VEC consecutive channels, from `c` on (D channels a
+// group): one division, then counted on.  UNI: VEC divides D, one group.
+template <int VEC, bool UNI, typename F>
+__device__ __forceinline__ void per_channel_group(int c, int D, F &&f) {
+    int g = c / D, left = D - (c - g * D);
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) {
+        f(q, g);
+        if (!UNI && --left == 0) {
+            left = D;
+            ++g;
+        }
+    }
+}
 
 struct GnTensor {
     const void *p;
@@ -43,93 +74,300 @@ struct GnParams {
     int64_t on, op;
     const float *gamma, *beta;
     float *mean, *rstd;                  // [N][G]
-    float *part;                         // [N][slabs][2][C]
-    float *coef;                         // [N][G][2] (backward)
+    float *part;                         // backward: [N][slabs][2][C] sums of dz and dz xhat
+    float *gpart;                        // two passes: [N][slabs][chunks * gpc][2] a group's (or piece's) sums
     float *ggamma, *gbeta;
     float eps;
     int32_t N, C, G, D, HW;
-    int32_t slabs, slab;                 // pixels per slab
-    int32_t tx, ty, col_blocks;          // threads along channel vectors and pixels; blocks along channels
     int32_t act;
-    int32_t chunks, gpc, splits, iters;  // on-chip form: channel chunks of gpc groups, CTAs of a cluster, slots a thread
+    // The split: channel chunks of gpc whole groups (or of 1 / pieces of one),
+    // tx vectors wide; slabs of pixels, a thread taking every ty-th; `seg` sums
+    // that a thread leaves for the groups of its vector (chip backward: threads
+    // that share a channel's sum).
+    int32_t chunks, gpc, pieces, width, tx, ty, slab, slabs, iters, threads, seg;
+    int32_t splits;                      // on-chip form: CTAs of a cluster
+    int32_t channel_blocks;              // backward, two passes: blocks that join the channels' sums
+    FastDiv fd_tx, fd_ty, fd_chunks, fd_slabs, fd_cb, fd_entries;
 };
 
-constexpr int kGnThreads = 256;
+constexpr int kGnThreads = 512;          // at most
 
-// The block's image, pixel slab and channels, and this thread's place in it.
+__device__ __forceinline__ float warp_sum_f(float v, int from = 16) {
+    for (int o = from; o > 0; o /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// VEC sums of a thread to shared memory, in wide stores: single words, VEC
+// apart, would meet VEC-fold bank conflicts.
 template <int VEC>
-struct GnPlace {
-    int n, slab, c, row, p0, p1;
-    bool on;
-    __device__ __forceinline__ explicit GnPlace(const GnParams &P) {
-        int b = blockIdx.x;
-        const int cb = b % P.col_blocks;
-        b /= P.col_blocks;
-        slab = b % P.slabs;
-        n = b / P.slabs;
-        row = threadIdx.x / P.tx;
-        c = (cb * P.tx + threadIdx.x % P.tx) * VEC;
-        on = row < P.ty && c < P.C;
-        p0 = slab * P.slab + row;
-        p1 = min(P.HW, (slab + 1) * P.slab);
+__device__ __forceinline__ void leave(float *at, const float (&v)[VEC]) {
+    if constexpr (VEC % 4 == 0) {
+#pragma unroll
+        for (int q = 0; q < VEC; q += 4)
+            *reinterpret_cast<float4 *>(at + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+    } else if constexpr (VEC == 2) {
+        *reinterpret_cast<float2 *>(at) = make_float2(v[0], v[1]);
+    } else {
+        at[0] = v[0];
+    }
+}
+
+// Sums over the CTA of f(channel of the thread's vector) by group, one warp a
+// group, given to out(group of the chunk, sum) in lane 0.  A thread leaves
+// seg values: one (UNI), VEC / D, or VEC; `per` of them belong to a group in
+// a row.  red: tx * ty * seg floats.
+template <int VEC, bool UNI, typename F, typename O>
+__device__ __forceinline__ void group_reduce(const GnParams &P, float *red, bool on, F &&f, O &&out) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    const int seg = UNI ? 1 : P.seg;
+    if (on) {
+        if (UNI || seg != VEC) {
+            const int len = VEC / seg;
+            float s = 0.f;
+            int at = threadIdx.x * seg, left = len;
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) {
+                s += f(q);
+                if (UNI ? q == VEC - 1 : --left == 0) {
+                    red[at++] = s;
+                    s = 0.f;
+                    left = len;
+                }
+            }
+        } else {
+            float v[VEC];
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) v[q] = f(q);
+            leave<VEC>(red + threadIdx.x * VEC, v);
+        }
+    }
+    __syncthreads();
+    const int per = P.fd_entries.d, total = per * P.ty, width = P.tx * seg;
+    for (int g = warp; g < P.gpc; g += warps) {
+        float s = 0.f;
+        for (int e = lane; e < total; e += 32) {
+            const int r = per == 1 ? e : P.fd_entries.div(e);
+            s += red[r * width + g * per + (e - r * per)];
+        }
+        s = warp_sum_f(s);
+        if (lane == 0) out(g, s);
+    }
+}
+
+// A thread's running statistics of its channels, about its first value of
+// each: that value being one of them, the difference of the squares loses at
+// most a factor of their number (never one of mean^2 / variance).
+template <int VEC>
+struct GnRunning {
+    float first[VEC], sum[VEC], sq[VEC];
+    __device__ __forceinline__ GnRunning() {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) first[q] = sum[q] = sq[q] = 0.f;
+    }
+    __device__ __forceinline__ void start(const float (&v)[VEC]) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) first[q] = -v[q];
+    }
+    __device__ __forceinline__ void add(float (&v)[VEC]) {
+        add_to(v, first);
+        add_to(sum, v);
+        fma_to(sq, v, v, sq);
+    }
+    // sum -> mean, sq -> squared deviations from it
+    __device__ __forceinline__ void finish(int count) {
+        const float inv = count > 0 ? 1.f / static_cast<float>(count) : 0.f;
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) {
+            const float d = sum[q] * inv;
+            sq[q] = fmaf(-sum[q], d, sq[q]);
+            sum[q] = d - first[q];
+        }
     }
 };
 
-// Per channel and slab: mean and sum of squared deviations, by Welford's
-// recurrence per thread (no difference of large squares), joined over the
-// block's pixel rows in row order (Chan et al.).
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kGnThreads) gn_stats_kernel(const __grid_constant__ GnParams P) {
-    __shared__ float sh[2][kGnThreads * VEC];
-    const GnPlace<VEC> at(P);
-    float mean[VEC] = {}, m2[VEC] = {};
-    if (at.on) {
-        const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c;
-        float k = 0.f;
-        constexpr int U = 4;
-        for (int p = at.p0; p < at.p1; p += U * P.ty) {
-            typename Pack<T, VEC>::Raw r[U];
+// Channels' sums joined over `rows` partial rows ([row][2][C]), 32 channels a
+// block, a warp every (blockDim / 32)-th row with four loads in flight; the
+// warps' shares in warp order.  sh: [warps][2][32] doubles.
+__device__ __forceinline__ void join_channels(const GnParams &P, int block, int64_t rows, double *sh) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+    const int c = block * 32 + lane;
+    double a = 0.0, b = 0.0;
+    if (c < P.C) {
+        const float *at = P.part + c;
+        for (int64_t e = warp; e < rows; e += 4 * warps) {
+            float va[4], vb[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t r = e + u * warps;
+                va[u] = r < rows ? at[r * 2 * P.C] : 0.f;
+                vb[u] = r < rows ? at[(r * 2 + 1) * P.C] : 0.f;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                a += va[u];
+                b += vb[u];
+            }
+        }
+    }
+    sh[(warp * 2) * 32 + lane] = a;
+    sh[(warp * 2 + 1) * 32 + lane] = b;
+    __syncthreads();
+    if (warp < 2 && c < P.C) {   // warp 0: gbeta, warp 1: ggamma
+        double s = 0.0;
+        for (int k = 0; k < warps; ++k) s += sh[(k * 2 + warp) * 32 + lane];
+        float *out = warp == 0 ? P.gbeta : P.ggamma;
+        if (out) out[c] = static_cast<float>(s);
+    }
+}
+static __global__ void __launch_bounds__(kGnThreads) gn_channels_kernel(const __grid_constant__ GnParams P,
+                                                                        int64_t rows) {
+    __shared__ double sh[kGnThreads / 32 * 2 * 32];
+    join_channels(P, blockIdx.x, rows, sh);
+}
+
+// Backward: the CTA's sums of dz (sa) and dz xhat (sb) by channel: csum[cb] and
+// csum[cb ..].  In two steps when there are threads to share a channel.  red:
+// 2 tx ty VEC floats, part: 2 blockDim, parts: threads that share a channel.
+template <int VEC>
+__device__ __forceinline__ void channel_sums(const GnParams &P, float *red, float *part, float *csum, bool on,
+                                             const float (&sa)[VEC], const float (&sb)[VEC]) {
+    const int threads = blockDim.x, nt = P.tx * P.ty, cb = P.tx * VEC;
+    float *redb = red + nt * VEC;
+    if (on) {
+        leave<VEC>(red + threadIdx.x * VEC, sa);
+        leave<VEC>(redb + threadIdx.x * VEC, sb);
+    }
+    __syncthreads();
+    if (cb <= threads / 2) {
+        const int parts = P.seg, at = P.fd_cb.div(threadIdx.x), ch = threadIdx.x - at * cb;
+        float s = 0.f, t = 0.f;
+        if (at < parts)
+            for (int r = at; r < P.ty; r += parts) {
+                s += red[r * cb + ch];
+                t += redb[r * cb + ch];
+            }
+        part[threadIdx.x] = s;
+        part[threads + threadIdx.x] = t;
+        __syncthreads();
+        for (int j = threadIdx.x; j < 2 * cb; j += threads) {
+            const int from = j >= cb ? threads + j - cb : j;
+            float v = 0.f;
+            for (int k = 0; k < parts; ++k) v += part[from + k * cb];
+            csum[j] = v;
+        }
+    } else {
+        for (int ch = threadIdx.x; ch < cb; ch += threads) {
+            float s = 0.f, t = 0.f;
+            for (int r = 0; r < P.ty; ++r) {
+                s += red[r * cb + ch];
+                t += redb[r * cb + ch];
+            }
+            csum[ch] = s;
+            csum[cb + ch] = t;
+        }
+    }
+    __syncthreads();
+}
+// Their sums times gamma over the `channels` of each of the chunk's groups,
+// one warp a group.  c0: the chunk's first channel.
+template <typename O>
+__device__ __forceinline__ void gamma_sums(const GnParams &P, const float *csum, int cb, int c0, int channels, O &&out) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    for (int g = warp; g < P.gpc; g += warps) {
+        float s = 0.f, t = 0.f;
+        for (int d = lane; d < channels; d += 32) {
+            const int k = g * P.D + d;
+            const float ga = P.gamma ? P.gamma[c0 + k] : 1.f;
+            s = fmaf(ga, csum[k], s);
+            t = fmaf(ga, csum[cb + k], t);
+        }
+        s = warp_sum_f(s);
+        t = warp_sum_f(t);
+        if (lane == 0) out(g, s, t);
+    }
+}
+
+// ---------------------------------------------------------------- two passes
+constexpr int kPassThreads = 256;
+
+// The block's image, slab and chunk, and this thread's place in it.
+template <int VEC>
+struct GnPlace {
+    int n, slab, chunk, row, col, c, p0, pixels, count, c_end;
+    bool on;
+    __device__ __forceinline__ GnPlace(const GnParams &P, int block) {
+        int b = P.fd_chunks.div(block);
+        chunk = block - b * P.chunks;
+        n = P.fd_slabs.div(b);
+        slab = b - n * P.slabs;
+        row = P.fd_tx.div(threadIdx.x);
+        col = threadIdx.x - row * P.tx;
+        // a piece of a group ends with the group
+        const int group = P.pieces > 1 ? chunk / P.pieces : chunk;
+        const int c0 = P.pieces > 1 ? group * P.D + (chunk - group * P.pieces) * P.width : chunk * P.width;
+        c_end = P.pieces > 1 ? min(c0 + P.width, (group + 1) * P.D) : c0 + P.width;
+        c = c0 + col * VEC;
+        on = row < P.ty && c < c_end;
+        const int first = slab * P.slab;
+        pixels = min(P.HW - first, P.slab);
+        p0 = first + row;
+        count = on && row < pixels ? P.fd_ty.div(pixels - row - 1) + 1 : 0;
+    }
+    // Channels of a group in this chunk, and the group's number in the image.
+    __device__ __forceinline__ int channels(const GnParams &P) const {
+        return P.pieces > 1 ? min(P.width, P.D - (chunk % P.pieces) * P.width) : P.D;
+    }
+    __device__ __forceinline__ int group(const GnParams &P, int g) const {
+        return P.pieces > 1 ? chunk / P.pieces : chunk * P.gpc + g;
+    }
+};
+
+// First pass: mean and squared deviations of each group (or piece) of the slab.
+template <typename T, int VEC, bool UNI>
+__global__ void __launch_bounds__(kPassThreads, 3) gn_stats_kernel(const __grid_constant__ GnParams P) {
+    extern __shared__ __align__(16) float gn_red[];
+    using V = Pack<T, VEC>;
+    const GnPlace<VEC> at(P, blockIdx.x);
+    GnRunning<VEC> run;
+    {
+        const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
+        const int64_t step = P.ty * P.x.sp;
+        constexpr int U = 8;
+        for (int i = 0; i < at.count; i += U) {
+            typename V::Raw r[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (p + u * P.ty < at.p1) r[u] = Pack<T, VEC>::load(x + (p + static_cast<int64_t>(u) * P.ty) * P.x.sp);
+                if (i + u < at.count) r[u] = V::load(x + u * step);
+            x += U * step;
+            if (i == 0) {
+                float v[VEC];
+                V::widen(r[0], v);
+                run.start(v);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (p + u * P.ty < at.p1) {
-                    k += 1.f;
-                    const float inv = __frcp_rn(k);
+                if (i + u < at.count) {
                     float v[VEC];
-                    Pack<T, VEC>::widen(r[u], v);
-#pragma unroll
-                    for (int q = 0; q < VEC; ++q) {
-                        const float d = v[q] - mean[q];
-                        mean[q] += d * inv;
-                        m2[q] += d * (v[q] - mean[q]);
-                    }
+                    V::widen(r[u], v);
+                    run.add(v);
                 }
         }
     }
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-        sh[0][threadIdx.x * VEC + q] = mean[q];
-        sh[1][threadIdx.x * VEC + q] = m2[q];
-    }
+    run.finish(at.count);
+    const int nt = P.tx * P.ty, seg = UNI ? 1 : P.seg;
+    float *mean = gn_red + nt * seg;
+    const float cnt = static_cast<float>(at.count);
+    const float total = static_cast<float>(at.pixels) * at.channels(P);
+    float2 *out = reinterpret_cast<float2 *>(P.gpart) +
+                  ((static_cast<int64_t>(at.n) * P.slabs + at.slab) * P.chunks + at.chunk) * P.gpc;
+    group_reduce<VEC, UNI>(P, gn_red, at.row < P.ty, [&](int q) { return cnt * run.sum[q]; },
+                           [&](int g, float s) { mean[g] = s / total; });
     __syncthreads();
-    // one thread per channel of the block; row t holds ceil((pixels - t) / ty)
-    const int pixels = at.p1 - at.slab * P.slab, width = P.tx * VEC;
-    const int c0 = (blockIdx.x % P.col_blocks) * width;
-    for (int i = threadIdx.x; i < width && c0 + i < P.C; i += kGnThreads) {
-        float n = 0.f, m = 0.f, s = 0.f;
-        for (int t = 0; t < P.ty && t < pixels; ++t) {
-            const float nt = static_cast<float>((pixels - t + P.ty - 1) / P.ty);
-            const float d = sh[0][t * width + i] - m, tot = n + nt;
-            m += d * (nt / tot);
-            s += sh[1][t * width + i] + d * d * (n * nt / tot);
-            n = tot;
-        }
-        float *out = P.part + (static_cast<int64_t>(at.n) * P.slabs + at.slab) * 2 * P.C + c0 + i;
-        out[0] = m;
-        out[P.C] = s;
-    }
+    float m[VEC];
+    per_channel_group<VEC, UNI>(at.col * VEC, P.D, [&](int q, int g) { m[q] = mean[g]; });
+    group_reduce<VEC, UNI>(P, gn_red, at.row < P.ty,
+                           [&](int q) { return fmaf(cnt * (run.sum[q] - m[q]), run.sum[q] - m[q], run.sq[q]); },
+                           [&](int g, float s) { out[g] = make_float2(mean[g], s); });
 }
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -138,229 +376,233 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// One warp per image and group: the partial statistics joined in double.
-static __global__ void __launch_bounds__(128) gn_finish_kernel(const __grid_constant__ GnParams P) {
-    const int64_t w = blockIdx.x * 4ll + threadIdx.x / 32;
-    if (w >= static_cast<int64_t>(P.N) * P.G) return;
-    const int lane = threadIdx.x % 32;
-    const int n = static_cast<int>(w / P.G), g = static_cast<int>(w % P.G);
-    const float *part = P.part + static_cast<int64_t>(n) * P.slabs * 2 * P.C + g * P.D;
-    const int64_t entries = static_cast<int64_t>(P.slabs) * P.D;
-    const double total = static_cast<double>(P.HW) * P.D;
-    double sum = 0.0, dev = 0.0;
-    for (int64_t e = lane; e < entries; e += 32) {
-        const int s = static_cast<int>(e / P.D), c = static_cast<int>(e % P.D);
-        const int cnt = min(P.HW, (s + 1) * P.slab) - s * P.slab;
-        sum += cnt * static_cast<double>(part[static_cast<int64_t>(s) * 2 * P.C + c]);
-    }
-    const double mean = warp_sum(sum) / total;
-    for (int64_t e = lane; e < entries; e += 32) {
-        const int s = static_cast<int>(e / P.D), c = static_cast<int>(e % P.D);
-        const int cnt = min(P.HW, (s + 1) * P.slab) - s * P.slab;
-        const double d = part[static_cast<int64_t>(s) * 2 * P.C + c] - mean;
-        dev += part[(static_cast<int64_t>(s) * 2 + 1) * P.C + c] + cnt * d * d;
-    }
-    dev = warp_sum(dev) / total;
-    if (lane == 0) {
-        P.mean[w] = static_cast<float>(mean);
-        P.rstd[w] = static_cast<float>(1.0 / sqrt(dev + P.eps));
+// The partial sums of group g of the block's chunk, over all slabs and pieces:
+// f(the pair, the values it covers), a lane every 32nd.
+template <int VEC, typename F>
+__device__ __forceinline__ void each_part(const GnParams &P, const GnPlace<VEC> &at, int g, F &&f) {
+    const float2 *part = reinterpret_cast<const float2 *>(P.gpart) + static_cast<int64_t>(at.n) * P.slabs * P.chunks * P.gpc;
+    const int first = P.pieces > 1 ? at.chunk - at.chunk % P.pieces : at.chunk;
+    for (int e = threadIdx.x % 32; e < P.slabs * P.pieces; e += 32) {
+        const int s = P.pieces > 1 ? e / P.pieces : e, k = e - s * P.pieces;
+        const int channels = P.pieces > 1 ? min(P.width, P.D - k * P.width) : P.D;
+        f(part[(static_cast<int64_t>(s) * P.chunks + first + k) * P.gpc + g],
+          static_cast<float>(min(P.HW - s * P.slab, P.slab)) * channels);
     }
 }
 
-// y = act((x - mean) (rstd gamma) + beta).
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kGnThreads) gn_apply_kernel(const __grid_constant__ GnParams P) {
-    const GnPlace<VEC> at(P);
-    if (!at.on) return;
-    float mean[VEC], a[VEC], b[VEC];
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-        const int64_t s = static_cast<int64_t>(at.n) * P.G + (at.c + q) / P.D;
-        mean[q] = P.mean[s];
-        a[q] = P.rstd[s] * (P.gamma ? P.gamma[at.c + q] : 1.f);
-        b[q] = P.beta ? P.beta[at.c + q] : 0.f;
-    }
-    const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c;
-    T *y = static_cast<T *>(P.out) + at.n * P.on + at.c;
+// Second pass: y = act((x - mean) (rstd gamma) + beta).  Blocks go from the
+// last image to the first, so that what the first pass read last is still in
+// L2.  The first loads are under way while the statistics are joined.
+template <typename T, int VEC, bool UNI>
+__global__ void __launch_bounds__(kPassThreads, 3) gn_apply_kernel(const __grid_constant__ GnParams P) {
+    extern __shared__ __align__(16) float gn_red[];
+    using V = Pack<T, VEC>;
+    const GnPlace<VEC> at(P, gridDim.x - 1 - blockIdx.x);
+    float *mean = gn_red, *rstd = gn_red + P.gpc;
+    const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
+    T *y = static_cast<T *>(P.out) + at.n * P.on + at.c + at.p0 * P.op;
+    const int64_t xstep = P.ty * P.x.sp, ystep = P.ty * P.op;
     constexpr int U = 4;
-    for (int p = at.p0; p < at.p1; p += U * P.ty) {
-        typename Pack<T, VEC>::Raw r[U];
+    typename V::Raw r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (p + u * P.ty < at.p1) r[u] = Pack<T, VEC>::load(x + (p + static_cast<int64_t>(u) * P.ty) * P.x.sp);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (p + u * P.ty < at.p1) {
-                float v[VEC];
-                Pack<T, VEC>::widen(r[u], v);
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) v[q] = (v[q] - mean[q]) * a[q] + b[q];
-                act_values(P.act, v);
-                Pack<T, VEC>::store(y + (p + static_cast<int64_t>(u) * P.ty) * P.op, v);
-            }
-    }
-}
-
-// Per channel and slab: sums of dz and dz xhat.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kGnThreads) gn_bwd_sums_kernel(const __grid_constant__ GnParams P) {
-    __shared__ float sh[2][kGnThreads * VEC];
-    const GnPlace<VEC> at(P);
-    float sa[VEC] = {}, sb[VEC] = {};
-    if (at.on) {
-        float mean[VEC], rstd[VEC], gamma[VEC], beta[VEC];
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-            const int64_t s = static_cast<int64_t>(at.n) * P.G + (at.c + q) / P.D;
-            mean[q] = P.mean[s];
-            rstd[q] = P.rstd[s];
-            gamma[q] = P.gamma ? P.gamma[at.c + q] : 1.f;
-            beta[q] = P.beta ? P.beta[at.c + q] : 0.f;
-        }
-        const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c;
-        const T *g = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c;
-        constexpr int U = 2;
-        for (int p = at.p0; p < at.p1; p += U * P.ty) {
-            typename Pack<T, VEC>::Raw rx[U], rg[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (p + u * P.ty < at.p1) {
-                    rx[u] = Pack<T, VEC>::load(x + (p + static_cast<int64_t>(u) * P.ty) * P.x.sp);
-                    rg[u] = Pack<T, VEC>::load(g + (p + static_cast<int64_t>(u) * P.ty) * P.g.sp);
-                }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (p + u * P.ty < at.p1) {
-                    float xv[VEC], gv[VEC];
-                    Pack<T, VEC>::widen(rx[u], xv);
-                    Pack<T, VEC>::widen(rg[u], gv);
-                    float z[VEC], sl[VEC];
-#pragma unroll
-                    for (int q = 0; q < VEC; ++q) {
-                        xv[q] = (xv[q] - mean[q]) * rstd[q];
-                        z[q] = xv[q] * gamma[q] + beta[q];
-                    }
-                    act_slopes(P.act, z, sl);
-#pragma unroll
-                    for (int q = 0; q < VEC; ++q) {
-                        const float dz = gv[q] * sl[q];
-                        sa[q] += dz;
-                        sb[q] += dz * xv[q];
-                    }
-                }
-        }
-    }
+    for (int u = 0; u < U; ++u)
+        if (u < at.count) r[u] = V::load(x + u * xstep);
+    float a[VEC], b[VEC], m[VEC];
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {
-        sh[0][threadIdx.x * VEC + q] = sa[q];
-        sh[1][threadIdx.x * VEC + q] = sb[q];
+        a[q] = P.gamma && at.on ? P.gamma[at.c + q] : 1.f;
+        b[q] = P.beta && at.on ? P.beta[at.c + q] : 0.f;
+    }
+    for (int g = threadIdx.x / 32; g < P.gpc; g += blockDim.x / 32) {
+        const double total = static_cast<double>(P.HW) * P.D;
+        double s = 0.0, dev = 0.0;
+        each_part(P, at, g, [&](float2 v, float n) { s += static_cast<double>(n) * v.x; });
+        const double mu = warp_sum(s) / total;
+        each_part(P, at, g, [&](float2 v, float n) { dev += v.y + n * (v.x - mu) * (v.x - mu); });
+        dev = warp_sum(dev) / total;
+        if (threadIdx.x % 32 == 0) {
+            mean[g] = static_cast<float>(mu);
+            rstd[g] = static_cast<float>(1.0 / sqrt(dev + P.eps));
+            if (at.slab == 0 && (P.pieces == 1 || at.chunk % P.pieces == 0)) {
+                const int64_t i = static_cast<int64_t>(at.n) * P.G + at.group(P, g);
+                P.mean[i] = mean[g];
+                P.rstd[i] = rstd[g];
+            }
+        }
     }
     __syncthreads();
-    const int width = P.tx * VEC, c0 = (blockIdx.x % P.col_blocks) * width;
-    for (int i = threadIdx.x; i < width && c0 + i < P.C; i += kGnThreads) {
-        float s = 0.f, t = 0.f;
-        for (int r = 0; r < P.ty; ++r) {
-            s += sh[0][r * width + i];
-            t += sh[1][r * width + i];
+    per_channel_group<VEC, UNI>(at.col * VEC, P.D, [&](int q, int g) {
+        m[q] = -mean[g];
+        a[q] *= rstd[g];
+    });
+    for (int i = 0; i < at.count; i += U) {
+        if (i > 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u < at.count) r[u] = V::load(x + u * xstep);
         }
-        float *out = P.part + (static_cast<int64_t>(at.n) * P.slabs + at.slab) * 2 * P.C + c0 + i;
-        out[0] = s;
-        out[P.C] = t;
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u < at.count) {
+                float v[VEC];
+                V::widen(r[u], v);
+                add_to(v, m);
+                fma_to(v, v, a, b);
+                act_values<true>(P.act, v);
+                V::store(y + u * ystep, v);
+            }
+        x += U * xstep;
+        y += U * ystep;
     }
 }
 
-// Blocks below `group_blocks`: one warp per image and group, S1 / (D HW) and
-// S2 / (D HW).  The others: 32 channels each, 4 warps over the images' and
-// slabs' partial sums, joined in a fixed order.
-static __global__ void __launch_bounds__(128) gn_bwd_finish_kernel(const __grid_constant__ GnParams P,
-                                                                   int32_t group_blocks) {
-    __shared__ double sh[4][2][32];
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    if (blockIdx.x < static_cast<unsigned>(group_blocks)) {
-        const int64_t w = blockIdx.x * 4ll + warp;
-        if (w >= static_cast<int64_t>(P.N) * P.G) return;
-        const int n = static_cast<int>(w / P.G), g = static_cast<int>(w % P.G);
-        const float *part = P.part + static_cast<int64_t>(n) * P.slabs * 2 * P.C + g * P.D;
-        const int64_t entries = static_cast<int64_t>(P.slabs) * P.D;
-        double s1 = 0.0, s2 = 0.0;
-        for (int64_t e = lane; e < entries; e += 32) {
-            const int64_t s = e / P.D;
-            const int c = static_cast<int>(e % P.D);
-            const double gamma = P.gamma ? P.gamma[g * P.D + c] : 1.f;
-            s1 += gamma * part[s * 2 * P.C + c];
-            s2 += gamma * part[(s * 2 + 1) * P.C + c];
+// What the backward pass keeps of a thread's channels.
+template <int VEC>
+struct GnSlope {
+    float mean[VEC], rstd[VEC], gamma[VEC], beta[VEC];
+    template <bool UNI>
+    __device__ __forceinline__ void load(const GnParams &P, int n, int group0, int inner, int c, bool on) {
+        per_channel_group<VEC, UNI>(on ? inner : 0, P.D, [&](int q, int g) {
+            const int64_t at = static_cast<int64_t>(n) * P.G + group0 + (on ? g : 0);
+            mean[q] = -P.mean[at];
+            rstd[q] = P.rstd[at];
+            gamma[q] = P.gamma && on ? P.gamma[c + q] : 1.f;
+            beta[q] = P.beta && on ? P.beta[c + q] : 0.f;
+        });
+    }
+    // x -> xhat, g -> dz
+    __device__ __forceinline__ void apply(int act, float (&x)[VEC], float (&g)[VEC]) const {
+        float z[VEC], sl[VEC];
+        add_to(x, mean);
+        mul_to(x, rstd);
+        fma_to(z, x, gamma, beta);
+        act_slopes<true>(act, z, sl);
+        mul_to(g, sl);
+    }
+};
+
+// First pass: sums of dz and dz xhat, by channel and (times gamma) by group.
+template <typename T, int VEC, bool UNI>
+__global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_sums_kernel(const __grid_constant__ GnParams P) {
+    extern __shared__ __align__(16) float gn_red[];
+    using V = Pack<T, VEC>;
+    const GnPlace<VEC> at(P, blockIdx.x);
+    const int group0 = at.group(P, 0);
+    GnSlope<VEC> K;
+    K.template load<UNI>(P, at.n, group0, at.col * VEC, at.c, at.on);
+    float sa[VEC] = {}, sb[VEC] = {};
+    {
+        const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
+        const T *g = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c + at.p0 * P.g.sp;
+        const int64_t xstep = P.ty * P.x.sp, gstep = P.ty * P.g.sp;
+        constexpr int U = 4;
+        for (int i = 0; i < at.count; i += U) {
+            typename V::Raw rx[U], rg[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u < at.count) {
+                    rx[u] = V::load(x + u * xstep);
+                    rg[u] = V::load(g + u * gstep);
+                }
+            x += U * xstep;
+            g += U * gstep;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i + u < at.count) {
+                    float xv[VEC], gv[VEC];
+                    V::widen(rx[u], xv);
+                    V::widen(rg[u], gv);
+                    K.apply(P.act, xv, gv);
+                    add_to(sa, gv);
+                    fma_to(sb, gv, xv, sb);
+                }
         }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (lane == 0) {
-            const double total = static_cast<double>(P.HW) * P.D;
-            P.coef[w * 2] = static_cast<float>(s1 / total);
-            P.coef[w * 2 + 1] = static_cast<float>(s2 / total);
-        }
+    }
+    const int nt = P.tx * P.ty, cb = P.tx * VEC, c0 = at.c - at.col * VEC;
+    float *part = gn_red + 2 * nt * VEC, *csum = part + 2 * blockDim.x;
+    channel_sums<VEC>(P, gn_red, part, csum, at.row < P.ty, sa, sb);
+    float *out = P.part + (static_cast<int64_t>(at.n) * P.slabs + at.slab) * 2 * P.C + c0;
+    for (int ch = threadIdx.x; ch < at.c_end - c0; ch += blockDim.x) {
+        out[ch] = csum[ch];
+        out[P.C + ch] = csum[cb + ch];
+    }
+    float2 *gout = reinterpret_cast<float2 *>(P.gpart) +
+                   ((static_cast<int64_t>(at.n) * P.slabs + at.slab) * P.chunks + at.chunk) * P.gpc;
+    gamma_sums(P, csum, cb, c0, at.channels(P), [&](int g, float s, float t) { gout[g] = make_float2(s, t); });
+}
+
+// Second pass: gx = rstd gamma dz - (rstd k1 + xhat rstd k2), from the last
+// image to the first.  The first channel_blocks blocks join the channels' sums
+// instead.
+template <typename T, int VEC, bool UNI>
+__global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_apply_kernel(const __grid_constant__ GnParams P) {
+    extern __shared__ __align__(16) float gn_red[];
+    using V = Pack<T, VEC>;
+    if (blockIdx.x < P.channel_blocks) {
+        join_channels(P, blockIdx.x, static_cast<int64_t>(P.N) * P.slabs, reinterpret_cast<double *>(gn_red));
         return;
     }
-    const int c = (blockIdx.x - group_blocks) * 32 + lane;
-    double a = 0.0, b = 0.0;
-    if (c < P.C)
-        for (int64_t e = warp; e < static_cast<int64_t>(P.N) * P.slabs; e += 4) {
-            a += P.part[e * 2 * P.C + c];
-            b += P.part[(e * 2 + 1) * P.C + c];
-        }
-    sh[warp][0][lane] = a;
-    sh[warp][1][lane] = b;
-    __syncthreads();
-    if (warp == 0 && c < P.C) {
-        if (P.gbeta) P.gbeta[c] = static_cast<float>((sh[0][0][lane] + sh[1][0][lane]) + (sh[2][0][lane] + sh[3][0][lane]));
-        if (P.ggamma) P.ggamma[c] = static_cast<float>((sh[0][1][lane] + sh[1][1][lane]) + (sh[2][1][lane] + sh[3][1][lane]));
-    }
-}
-
-// gx = rstd (gamma dz - k1 - xhat k2).
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kGnThreads) gn_bwd_apply_kernel(const __grid_constant__ GnParams P) {
-    const GnPlace<VEC> at(P);
-    if (!at.on) return;
-    float mean[VEC], rstd[VEC], gamma[VEC], beta[VEC], k1[VEC], k2[VEC];
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-        const int64_t s = static_cast<int64_t>(at.n) * P.G + (at.c + q) / P.D;
-        mean[q] = P.mean[s];
-        rstd[q] = P.rstd[s];
-        gamma[q] = P.gamma ? P.gamma[at.c + q] : 1.f;
-        beta[q] = P.beta ? P.beta[at.c + q] : 0.f;
-        k1[q] = P.coef[s * 2];
-        k2[q] = P.coef[s * 2 + 1];
-    }
-    const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c;
-    const T *g = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c;
-    T *o = static_cast<T *>(P.out) + at.n * P.on + at.c;
+    const GnPlace<VEC> at(P, gridDim.x - 1 - blockIdx.x);
+    const int group0 = at.group(P, 0);
+    float *k1 = gn_red, *k2 = gn_red + P.gpc;
+    const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
+    const T *g = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c + at.p0 * P.g.sp;
+    T *o = static_cast<T *>(P.out) + at.n * P.on + at.c + at.p0 * P.op;
+    const int64_t xstep = P.ty * P.x.sp, gstep = P.ty * P.g.sp, ostep = P.ty * P.op;
     constexpr int U = 2;
-    for (int p = at.p0; p < at.p1; p += U * P.ty) {
-        typename Pack<T, VEC>::Raw rx[U], rg[U];
+    typename V::Raw rx[U], rg[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (p + u * P.ty < at.p1) {
-                rx[u] = Pack<T, VEC>::load(x + (p + static_cast<int64_t>(u) * P.ty) * P.x.sp);
-                rg[u] = Pack<T, VEC>::load(g + (p + static_cast<int64_t>(u) * P.ty) * P.g.sp);
-            }
+    for (int u = 0; u < U; ++u)
+        if (u < at.count) {
+            rx[u] = V::load(x + u * xstep);
+            rg[u] = V::load(g + u * gstep);
+        }
+    GnSlope<VEC> K;
+    K.template load<UNI>(P, at.n, group0, at.col * VEC, at.c, at.on);
+    for (int j = threadIdx.x / 32; j < P.gpc; j += blockDim.x / 32) {
+        const double total = static_cast<double>(P.HW) * P.D;
+        double s = 0.0, t = 0.0;
+        each_part(P, at, j, [&](float2 v, float) {
+            s += v.x;
+            t += v.y;
+        });
+        s = warp_sum(s);
+        t = warp_sum(t);
+        if (threadIdx.x % 32 == 0) {
+            k1[j] = static_cast<float>(s / total);
+            k2[j] = static_cast<float>(t / total);
+        }
+    }
+    __syncthreads();
+    float scale[VEC], c1[VEC], c2[VEC];
+    per_channel_group<VEC, UNI>(at.col * VEC, P.D, [&](int q, int j) {
+        scale[q] = K.rstd[q] * K.gamma[q];
+        c1[q] = -K.rstd[q] * k1[j];
+        c2[q] = -K.rstd[q] * k2[j];
+    });
+    for (int i = 0; i < at.count; i += U) {
+        if (i > 0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (p + u * P.ty < at.p1) {
-                float xv[VEC], gv[VEC];
-                Pack<T, VEC>::widen(rx[u], xv);
-                Pack<T, VEC>::widen(rg[u], gv);
-                float z[VEC], sl[VEC];
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) {
-                    xv[q] = (xv[q] - mean[q]) * rstd[q];
-                    z[q] = xv[q] * gamma[q] + beta[q];
+            for (int u = 0; u < U; ++u)
+                if (i + u < at.count) {
+                    rx[u] = V::load(x + u * xstep);
+                    rg[u] = V::load(g + u * gstep);
                 }
-                act_slopes(P.act, z, sl);
+        }
 #pragma unroll
-                for (int q = 0; q < VEC; ++q)
-                    xv[q] = rstd[q] * (gamma[q] * gv[q] * sl[q] - k1[q] - xv[q] * k2[q]);
-                Pack<T, VEC>::store(o + (p + static_cast<int64_t>(u) * P.ty) * P.op, xv);
+        for (int u = 0; u < U; ++u)
+            if (i + u < at.count) {
+                float xv[VEC], gv[VEC];
+                V::widen(rx[u], xv);
+                V::widen(rg[u], gv);
+                K.apply(P.act, xv, gv);
+                fma_to(xv, xv, c2, c1);
+                fma_to(gv, gv, scale, xv);
+                V::store(o + u * ostep, gv);
             }
+        x += U * xstep;
+        g += U * gstep;
+        o += U * ostep;
     }
 }
 
@@ -384,106 +626,62 @@ __device__ __forceinline__ void gn_cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 template <int BYTES>
-__device__ __forceinline__ void gn_copy_async(void *dst, const void *src) {
+__device__ __forceinline__ void gn_copy_async(uint32_t dst, const void *src) {
     if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void gn_copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+__device__ __forceinline__ uint32_t gn_cluster_id() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+
 // The tensor read once: a cluster of CTAs holds one image's chunk of whole
 // groups on chip, each CTA a slab of its pixels.  A thread copies the vectors
 // it will work on (fixed channels, every ty-th pixel) into its own slots of
-// shared memory, all copies in flight at once, and reads them again for each
-// pass; so no pass but the sums meets a barrier.  Sums go over the CTA's rows
-// in shared memory and over the cluster through distributed shared memory,
-// always in the same order.
+// shared memory, all copies in flight at once, and reads them again for the
+// second pass; so only the sums meet barriers.  Sums go over the CTA in shared
+// memory and over the cluster through distributed shared memory, always in the
+// same order.
 template <typename T, int VEC>
 struct GnChip {
     static constexpr int kBytes = VEC * sizeof(T);
     const GnParams &P;
-    int n, chunk, rank, col, row, nt, cb, c, p0, count;
+    int n, chunk, rank, col, row, nt, cb, c, p0, count, pixels;
     bool on;
     T *xs, *gs;
-    float *red, *part, *csum, *group;     // [nt][VEC], [256], [cb] x 2, [gpc] x 4
+    float *red;                          // row sums
 
     __device__ __forceinline__ GnChip(const GnParams &p, uint8_t *smem, bool two) : P(p) {
-        int b = blockIdx.x;
-        rank = b % P.splits;
-        b /= P.splits;
-        chunk = b % P.chunks;
-        n = b / P.chunks;
-        col = threadIdx.x % P.tx;
-        row = threadIdx.x / P.tx;
+        const int id = gn_cluster_id();
+        rank = gn_cluster_rank();
+        n = P.fd_chunks.div(id);
+        chunk = id - n * P.chunks;
+        row = P.fd_tx.div(threadIdx.x);
+        col = threadIdx.x - row * P.tx;
         nt = P.tx * P.ty;
         cb = P.tx * VEC;
         c = chunk * cb + col * VEC;
         on = row < P.ty;
-        p0 = rank * P.slab + row;
-        const int p1 = min(P.HW, (rank + 1) * P.slab);
-        count = on && p0 < p1 ? (p1 - p0 + P.ty - 1) / P.ty : 0;
+        const int first = rank * P.slab;
+        pixels = min(P.HW - first, P.slab);
+        p0 = first + row;
+        count = on && row < pixels ? P.fd_ty.div(pixels - row - 1) + 1 : 0;
         xs = reinterpret_cast<T *>(smem) + threadIdx.x * VEC;
-        uint8_t *end = smem + static_cast<size_t>(P.iters) * nt * kBytes;
-        gs = nullptr;
-        if (two) {
-            gs = reinterpret_cast<T *>(end) + threadIdx.x * VEC;
-            end += static_cast<size_t>(P.iters) * nt * kBytes;
-        }
-        red = reinterpret_cast<float *>(smem + (((end - smem) + 15) & ~static_cast<size_t>(15)));
-        part = red + nt * VEC;
-        csum = part + kGnThreads;
-        group = csum + 2 * cb;
+        const int bytes = P.iters * nt * kBytes;
+        gs = reinterpret_cast<T *>(smem + bytes) + threadIdx.x * VEC;
+        red = reinterpret_cast<float *>(smem + ((bytes * (two ? 2 : 1) + 15) & ~15));
     }
-    __device__ __forceinline__ const T *slot(const T *base, int i) const { return base + i * nt * VEC; }
-    __device__ __forceinline__ T *slot(T *base, int i) const { return base + i * nt * VEC; }
-
-    // Sums of v over the CTA's rows: csum[channel of the chunk].
-    __device__ __forceinline__ void channel_sums(const float (&v)[VEC], float *out) {
-        if (on)
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) red[threadIdx.x * VEC + q] = v[q];
-        __syncthreads();
-        if (cb <= kGnThreads / 2) {
-            const int parts = kGnThreads / cb, at = threadIdx.x / cb, ch = threadIdx.x - at * cb;
-            float s = 0.f;
-            if (at < parts)
-                for (int r = at; r < P.ty; r += parts) s += red[r * cb + ch];
-            part[threadIdx.x] = s;
-            __syncthreads();
-            if (threadIdx.x < cb) {
-                s = 0.f;
-                for (int k = 0; k < parts; ++k) s += part[k * cb + threadIdx.x];
-                out[threadIdx.x] = s;
-            }
-        } else {
-            for (int ch = threadIdx.x; ch < cb; ch += kGnThreads) {
-                float s = 0.f;
-                for (int r = 0; r < P.ty; ++r) s += red[r * cb + ch];
-                out[ch] = s;
-            }
-        }
-        __syncthreads();
-    }
-    // Sums of the channel sums over each group (times gamma), one warp a group.
-    __device__ __forceinline__ void group_sums(const float *ch, const float *gamma, float *out) {
-        const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-        for (int g = warp; g < P.gpc; g += kGnThreads / 32) {
-            float s = 0.f;
-            for (int d = lane; d < P.D; d += 32) {
-                const int k = g * P.D + d;
-                s += gamma ? gamma[chunk * cb + k] * ch[k] : ch[k];
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            if (lane == 0) out[g] = s;
-        }
-    }
-    // Everyone's `p` is written and may be read by the cluster.
-    __device__ __forceinline__ void meet() {
+    __device__ __forceinline__ int quarter(int k) const { return min(count, (k * P.iters + 3) / 4); }
+    // Everyone's sums are written and may be read by the cluster.
+    __device__ __forceinline__ void meet() const {
         if (P.splits > 1) {
             gn_cluster_arrive();
             gn_cluster_wait();
@@ -491,197 +689,228 @@ struct GnChip {
             __syncthreads();
         }
     }
-    __device__ __forceinline__ float over_cluster(const float *p) const {
-        if (P.splits == 1) return *p;
-        float s = 0.f;
-        for (int r = 0; r < P.splits; ++r) s += gn_ld_rank(p, r);
-        return s;
-    }
 };
 
-template <typename T, int VEC>
+// The CTA joins its threads, and the cluster its CTAs, by means and squared
+// deviations (Chan et al.).
+template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kGnThreads) gn_chip_fwd_kernel(const __grid_constant__ GnParams P) {
     extern __shared__ __align__(16) uint8_t gn_smem[];
+    using V = Pack<T, VEC>;
     GnChip<T, VEC> K(P, gn_smem, false);
-    const T *x = static_cast<const T *>(P.x.p) + K.n * P.x.sn + K.c;
-    // four groups of copies, summed as they land
-    const int quarter = (P.iters + 3) / 4;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+    const int seg = UNI ? 1 : P.seg;
+    float *sums = K.red + K.nt * seg;            // [gpc] x 4: CTA's means, squares; mean, rstd
+    float *dev = sums + P.gpc, *mean = dev + P.gpc, *rstd = mean + P.gpc;
+    const int stride = K.nt * VEC;               // between a thread's slots
+    {
+        const T *x = static_cast<const T *>(P.x.p) + K.n * P.x.sn + K.c + K.p0 * P.x.sp;
+        const int64_t step = P.ty * P.x.sp;
+        uint32_t dst = smem_u32(K.xs);
+        // four groups of copies, summed as they land
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int end = min(K.count, (k + 1) * quarter);
-        for (int i = k * quarter; i < end; ++i)
-            gn_copy_async<K.kBytes>(K.slot(K.xs, i), x + (K.p0 + static_cast<int64_t>(i) * P.ty) * P.x.sp);
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int k = 0; k < 4; ++k) {
+            const int end = K.quarter(k + 1);
+            for (int i = K.quarter(k); i < end; ++i) {
+                gn_copy_async<K.kBytes>(dst, x);
+                x += step;
+                dst += stride * sizeof(T);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
     }
-    float acc[VEC] = {};
+    float a[VEC], b[VEC];
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) {
+        a[q] = P.gamma && K.on ? P.gamma[K.c + q] : 1.f;
+        b[q] = P.beta && K.on ? P.beta[K.c + q] : 0.f;
+    }
+    GnRunning<VEC> run;
+    const T *slot = K.xs;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         if (k == 0) gn_copy_wait<3>();
         if (k == 1) gn_copy_wait<2>();
         if (k == 2) gn_copy_wait<1>();
         if (k == 3) gn_copy_wait<0>();
-        const int end = min(K.count, (k + 1) * quarter);
-        for (int i = k * quarter; i < end; ++i) {
+        if (k == 0 && K.count > 0) {
             float v[VEC];
-            Pack<T, VEC>::widen(Pack<T, VEC>::load(K.slot(K.xs, i)), v);
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) acc[q] += v[q];
+            V::widen(V::load(slot), v);
+            run.start(v);
+        }
+        const int end = K.quarter(k + 1);
+#pragma unroll 2
+        for (int i = K.quarter(k); i < end; ++i, slot += stride) {
+            float v[VEC];
+            V::widen(V::load(slot), v);
+            run.add(v);
         }
     }
-    const float total = static_cast<float>(P.HW) * P.D;
-    K.channel_sums(acc, K.csum);
-    K.group_sums(K.csum, nullptr, K.group);
-    K.meet();
-    float *mean = K.group + 2 * P.gpc, *rstd = mean + P.gpc;
-    for (int g = threadIdx.x; g < P.gpc; g += kGnThreads) mean[g] = K.over_cluster(K.group + g) / total;
+    run.finish(K.count);
+    const float cnt = static_cast<float>(K.count);
+    const float here = static_cast<float>(K.pixels) * P.D;
+    group_reduce<VEC, UNI>(P, K.red, K.on, [&](int q) { return cnt * run.sum[q]; },
+                           [&](int g, float s) { sums[g] = s / here; });
     __syncthreads();
     float m[VEC];
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-        m[q] = mean[(K.col * VEC + q) / P.D];
-        acc[q] = 0.f;
-    }
-    for (int i = 0; i < K.count; ++i) {
-        float v[VEC];
-        Pack<T, VEC>::widen(Pack<T, VEC>::load(K.slot(K.xs, i)), v);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) {
-            const float d = v[q] - m[q];
-            acc[q] = fmaf(d, d, acc[q]);
-        }
-    }
-    K.channel_sums(acc, K.csum);
-    K.group_sums(K.csum, nullptr, K.group + P.gpc);
+    per_channel_group<VEC, UNI>(K.col * VEC, P.D, [&](int q, int g) { m[q] = sums[g]; });
+    group_reduce<VEC, UNI>(P, K.red, K.on,
+                           [&](int q) { return fmaf(cnt * (run.sum[q] - m[q]), run.sum[q] - m[q], run.sq[q]); },
+                           [&](int g, float s) { dev[g] = s; });
     K.meet();
-    for (int g = threadIdx.x; g < P.gpc; g += kGnThreads) {
-        const float r = 1.f / sqrtf(K.over_cluster(K.group + P.gpc + g) / total + P.eps);
-        rstd[g] = r;
-        if (K.rank == 0) {
-            const int64_t at = static_cast<int64_t>(K.n) * P.G + K.chunk * P.gpc + g;
-            P.mean[at] = mean[g];
-            P.rstd[at] = r;
+    const float total = static_cast<float>(P.HW) * P.D;
+    for (int g = warp; g < P.gpc; g += warps) {
+        float mu = sums[g], s2 = dev[g];
+        if (P.splits > 1) {   // one lane a CTA
+            const bool in = lane < P.splits;
+            const float n = in ? static_cast<float>(min(P.HW - lane * P.slab, P.slab)) * P.D : 0.f;
+            const float mr = in ? gn_ld_rank(sums + g, lane) : 0.f, sr = in ? gn_ld_rank(dev + g, lane) : 0.f;
+            // about the first CTA's mean, so that equal means stay exact
+            const float base = __shfl_sync(0xFFFFFFFFu, mr, 0);
+            mu = base + warp_sum_f(in ? n * (mr - base) : 0.f, 8) / total;
+            mu = __shfl_sync(0xFFFFFFFFu, mu, 0);
+            s2 = warp_sum_f(in ? fmaf(n * (mr - mu), mr - mu, sr) : 0.f, 8);
+        }
+        if (lane == 0) {
+            const float r = 1.f / sqrtf(s2 / total + P.eps);
+            mean[g] = mu;
+            rstd[g] = r;
+            if (K.rank == 0) {
+                const int64_t at = static_cast<int64_t>(K.n) * P.G + K.chunk * P.gpc + g;
+                P.mean[at] = mu;
+                P.rstd[at] = r;
+            }
         }
     }
     if (P.splits > 1) gn_cluster_arrive();   // the last remote read is done
     __syncthreads();
-    float a[VEC], b[VEC];
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-        a[q] = rstd[(K.col * VEC + q) / P.D] * (P.gamma && K.on ? P.gamma[K.c + q] : 1.f);
-        b[q] = P.beta && K.on ? P.beta[K.c + q] : 0.f;
-    }
-    T *y = static_cast<T *>(P.out) + K.n * P.on + K.c;
-    for (int i = 0; i < K.count; ++i) {
+    per_channel_group<VEC, UNI>(K.col * VEC, P.D, [&](int q, int g) {
+        m[q] = -mean[g];
+        a[q] *= rstd[g];
+    });
+    T *y = static_cast<T *>(P.out) + K.n * P.on + K.c + K.p0 * P.op;
+    const int64_t step = P.ty * P.op;
+    slot = K.xs;
+#pragma unroll 2
+    for (int i = 0; i < K.count; ++i, slot += stride, y += step) {
         float v[VEC];
-        Pack<T, VEC>::widen(Pack<T, VEC>::load(K.slot(K.xs, i)), v);
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) v[q] = (v[q] - m[q]) * a[q] + b[q];
-        act_values(P.act, v);
-        Pack<T, VEC>::store(y + (K.p0 + static_cast<int64_t>(i) * P.ty) * P.op, v);
+        V::widen(V::load(slot), v);
+        add_to(v, m);
+        fma_to(v, v, a, b);
+        act_values<true>(P.act, v);
+        V::store(y, v);
     }
     if (P.splits > 1) gn_cluster_wait();
 }
 
-template <typename T, int VEC>
+// Backward.
+template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kGnThreads) gn_chip_bwd_kernel(const __grid_constant__ GnParams P) {
     extern __shared__ __align__(16) uint8_t gn_smem[];
+    using V = Pack<T, VEC>;
     GnChip<T, VEC> K(P, gn_smem, true);
-    const T *x = static_cast<const T *>(P.x.p) + K.n * P.x.sn + K.c;
-    const T *g = static_cast<const T *>(P.g.p) + K.n * P.g.sn + K.c;
-    const int quarter = (P.iters + 3) / 4;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32, threads = blockDim.x;
+    float *part = K.red + 2 * K.nt * VEC;        // [threads] x 2
+    float *csum = part + 2 * threads;            // [cb] x 2: channel sums of dz and dz xhat
+    float *gsum = csum + 2 * K.cb;               // [gpc] x 2: their group sums times gamma
+    float *k1 = gsum + 2 * P.gpc, *k2 = k1 + P.gpc;
+    const int stride = K.nt * VEC;
+    {
+        const T *x = static_cast<const T *>(P.x.p) + K.n * P.x.sn + K.c + K.p0 * P.x.sp;
+        const T *g = static_cast<const T *>(P.g.p) + K.n * P.g.sn + K.c + K.p0 * P.g.sp;
+        const int64_t xstep = P.ty * P.x.sp, gstep = P.ty * P.g.sp;
+        uint32_t xd = smem_u32(K.xs), gd = smem_u32(K.gs);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int end = min(K.count, (k + 1) * quarter);
-        for (int i = k * quarter; i < end; ++i) {
-            const int64_t p = K.p0 + static_cast<int64_t>(i) * P.ty;
-            gn_copy_async<K.kBytes>(K.slot(K.xs, i), x + p * P.x.sp);
-            gn_copy_async<K.kBytes>(K.slot(K.gs, i), g + p * P.g.sp);
+        for (int k = 0; k < 4; ++k) {
+            const int end = K.quarter(k + 1);
+            for (int i = K.quarter(k); i < end; ++i) {
+                gn_copy_async<K.kBytes>(xd, x);
+                gn_copy_async<K.kBytes>(gd, g);
+                x += xstep;
+                g += gstep;
+                xd += stride * sizeof(T);
+                gd += stride * sizeof(T);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    float mean[VEC], rstd[VEC], gamma[VEC], beta[VEC];
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-        const int64_t at = static_cast<int64_t>(K.n) * P.G + (K.on ? (K.c + q) / P.D : 0);
-        mean[q] = P.mean[at];
-        rstd[q] = P.rstd[at];
-        gamma[q] = P.gamma && K.on ? P.gamma[K.c + q] : 1.f;
-        beta[q] = P.beta && K.on ? P.beta[K.c + q] : 0.f;
-    }
+    GnSlope<VEC> S;
+    S.template load<UNI>(P, K.n, 0, K.c, K.c, K.on);
     float sa[VEC] = {}, sb[VEC] = {};
+    T *xs = K.xs, *gs = K.gs;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         if (k == 0) gn_copy_wait<3>();
         if (k == 1) gn_copy_wait<2>();
         if (k == 2) gn_copy_wait<1>();
         if (k == 3) gn_copy_wait<0>();
-        const int end = min(K.count, (k + 1) * quarter);
-        for (int i = k * quarter; i < end; ++i) {
-            float xv[VEC], gv[VEC], z[VEC], sl[VEC];
-            Pack<T, VEC>::widen(Pack<T, VEC>::load(K.slot(K.xs, i)), xv);
-            Pack<T, VEC>::widen(Pack<T, VEC>::load(K.slot(K.gs, i)), gv);
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) {
-                xv[q] = (xv[q] - mean[q]) * rstd[q];
-                z[q] = xv[q] * gamma[q] + beta[q];
-            }
-            act_slopes(P.act, z, sl);
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) {
-                gv[q] *= sl[q];
-                sa[q] += gv[q];
-                sb[q] += gv[q] * xv[q];
-            }
+        const int end = K.quarter(k + 1);
+#pragma unroll 1
+        for (int i = K.quarter(k); i < end; ++i, xs += stride, gs += stride) {
+            float xv[VEC], gv[VEC];
+            V::widen(V::load(xs), xv);
+            V::widen(V::load(gs), gv);
+            S.apply(P.act, xv, gv);
+            add_to(sa, gv);
+            fma_to(sb, gv, xv, sb);
             if constexpr (sizeof(T) == 4) {   // xhat and dz in the slots: not computed again
-                Pack<T, VEC>::store(K.slot(K.xs, i), xv);
-                Pack<T, VEC>::store(K.slot(K.gs, i), gv);
+                V::store(xs, xv);
+                V::store(gs, gv);
             }
         }
     }
-    K.channel_sums(sa, K.csum);
-    K.channel_sums(sb, K.csum + K.cb);
-    K.group_sums(K.csum, P.gamma, K.group);
-    K.group_sums(K.csum + K.cb, P.gamma, K.group + P.gpc);
+    channel_sums<VEC>(P, K.red, part, csum, K.on, sa, sb);
+    gamma_sums(P, csum, K.cb, K.chunk * K.cb, P.D, [&](int g, float s, float t) {
+        gsum[g] = s;
+        gsum[P.gpc + g] = t;
+    });
     K.meet();
     const float total = static_cast<float>(P.HW) * P.D;
-    float *k1 = K.group + 2 * P.gpc, *k2 = k1 + P.gpc;
-    for (int j = threadIdx.x; j < P.gpc; j += kGnThreads) {
-        k1[j] = K.over_cluster(K.group + j) / total;
-        k2[j] = K.over_cluster(K.group + P.gpc + j) / total;
+    for (int g = warp; g < 2 * P.gpc; g += warps) {
+        float s = gsum[g];
+        if (P.splits > 1) s = warp_sum_f(lane < P.splits ? gn_ld_rank(gsum + g, lane) : 0.f, 8);
+        if (lane == 0) k1[g] = s / total;        // k2 follows k1
     }
     // the image's channel sums, for ggamma and gbeta: each CTA its share
     float *out = P.part + static_cast<int64_t>(K.n) * 2 * P.C + K.chunk * K.cb;
-    for (int ch = threadIdx.x * P.splits + K.rank; ch < K.cb; ch += kGnThreads * P.splits) {
-        out[ch] = K.over_cluster(K.csum + ch);
-        out[P.C + ch] = K.over_cluster(K.csum + K.cb + ch);
+    for (int ch = threadIdx.x * P.splits + K.rank; ch < K.cb; ch += threads * P.splits) {
+        float s = 0.f, t = 0.f;
+        if (P.splits == 1) {
+            s = csum[ch];
+            t = csum[K.cb + ch];
+        } else {
+            for (int r = 0; r < P.splits; r += 2) {   // an even number of CTAs
+                const float s0 = gn_ld_rank(csum + ch, r), s1 = gn_ld_rank(csum + ch, r + 1);
+                const float t0 = gn_ld_rank(csum + K.cb + ch, r), t1 = gn_ld_rank(csum + K.cb + ch, r + 1);
+                s += s0 + s1;
+                t += t0 + t1;
+            }
+        }
+        out[ch] = s;
+        out[P.C + ch] = t;
     }
     if (P.splits > 1) gn_cluster_arrive();
     __syncthreads();
-    float c1[VEC], c2[VEC];
-#pragma unroll
-    for (int q = 0; q < VEC; ++q) {
-        c1[q] = k1[(K.col * VEC + q) / P.D];
-        c2[q] = k2[(K.col * VEC + q) / P.D];
-    }
-    T *o = static_cast<T *>(P.out) + K.n * P.on + K.c;
-    for (int i = 0; i < K.count; ++i) {
+    // gx = rstd gamma dz - (rstd k1 + xhat rstd k2); sa, sb: the last two
+    float scale[VEC];
+    per_channel_group<VEC, UNI>(K.col * VEC, P.D, [&](int q, int g) {
+        scale[q] = S.rstd[q] * S.gamma[q];
+        sa[q] = -S.rstd[q] * k1[g];
+        sb[q] = -S.rstd[q] * k2[g];
+    });
+    T *o = static_cast<T *>(P.out) + K.n * P.on + K.c + K.p0 * P.op;
+    const int64_t step = P.ty * P.op;
+    xs = K.xs;
+    gs = K.gs;
+#pragma unroll 1
+    for (int i = 0; i < K.count; ++i, xs += stride, gs += stride, o += step) {
         float xv[VEC], gv[VEC];
-        Pack<T, VEC>::widen(Pack<T, VEC>::load(K.slot(K.xs, i)), xv);
-        Pack<T, VEC>::widen(Pack<T, VEC>::load(K.slot(K.gs, i)), gv);
-        if constexpr (sizeof(T) != 4) {
-            float z[VEC], sl[VEC];
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) {
-                xv[q] = (xv[q] - mean[q]) * rstd[q];
-                z[q] = xv[q] * gamma[q] + beta[q];
-            }
-            act_slopes(P.act, z, sl);
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) gv[q] *= sl[q];
-        }
-#pragma unroll
-        for (int q = 0; q < VEC; ++q) gv[q] = rstd[q] * (gamma[q] * gv[q] - c1[q] - xv[q] * c2[q]);
-        Pack<T, VEC>::store(o + (K.p0 + static_cast<int64_t>(i) * P.ty) * P.op, gv);
+        V::widen(V::load(xs), xv);
+        V::widen(V::load(gs), gv);
+        if constexpr (sizeof(T) != 4) S.apply(P.act, xv, gv);
+        fma_to(xv, xv, sb, sa);
+        fma_to(gv, gv, scale, xv);
+        V::store(o, gv);
     }
     if (P.splits > 1) gn_cluster_wait();
 }

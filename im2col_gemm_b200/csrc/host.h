@@ -6,7 +6,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/mqc.h"
+#include "common.cuh"
 
 namespace mqc {
 
@@ -36,6 +39,15 @@ mqc_status encode_matrix_map(CUtensorMap *map, const void *base, int64_t rows, i
 // Reads and clears the device error word of the linear kernels (each
 // translation unit has its own word).
 cudaError_t linear_take_device_error(int *value);
+
+inline FastDiv make_fastdiv(int32_t d) {
+    FastDiv f;
+    f.d = static_cast<uint32_t>(std::max(1, d));
+    f.l = 0;
+    while ((1ull << f.l) < f.d) ++f.l;
+    f.m = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.l) - f.d)) / f.d + 1);
+    return f;
+}
 
 inline bool act_ok(int act) { return act >= MQC_ACT_NONE && act <= MQC_ACT_GELU; }
 inline int dtype_bytes(int dtype) { return dtype == MQC_F32 ? 4 : 2; }

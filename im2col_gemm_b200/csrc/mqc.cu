@@ -292,15 +292,6 @@ uint32_t mma_fmt(int f) { return f == MQC_E4M3 ? 0u : (f == MQC_E5M2 ? 1u : 5u);
 
 const uint64_t kDefaultTimeoutNs = 4000000000ull;
 
-FastDiv make_fastdiv(int32_t d) {
-    FastDiv f;
-    f.d = static_cast<uint32_t>(std::max(1, d));
-    f.l = 0;
-    while ((1ull << f.l) < f.d) ++f.l;
-    f.m = static_cast<uint32_t>(((1ull << 32) * ((1ull << f.l) - f.d)) / f.d + 1);
-    return f;
-}
-
 template <int KIND>
 mqc_status launch_gemm(GemmParams &P, const DevInfo &d, cudaStream_t stream) {
     // CONV: the weights' scale atoms are the same for every output tile of a
