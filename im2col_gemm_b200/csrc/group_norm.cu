@@ -96,9 +96,8 @@ bool search_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
                                      chip_extra(tx, ty, vec, P.D, gpc, threads, bwd);
                 if (need > kChipSmem || slab * (splits - 1) >= P.HW) continue;
                 const int64_t ctas = int64_t(P.N) * (P.G / gpc) * splits;
-                const int64_t regs = bwd && vec == 8 ? 104 : 64;
                 const int64_t resident = std::max<int64_t>(
-                    1, std::min({ceil_div(ctas, 148), 65536 / (threads * regs), (228 * 1024) / (need + 1024)}));
+                    1, std::min({ceil_div(ctas, 148), int64_t(1024 / threads), (228 * 1024) / (need + 1024)}));
                 const double bytes = resident * double(slab) * row * waste / 43.0;
                 const double warps = resident * threads / 128.0;
                 const double issued = warps * (300.0 + iters * vec * (bwd ? 26.0 : 14.0)) /
@@ -157,9 +156,10 @@ bool plan_chip(GnParams &P, int vec, int32_t dtype, bool bwd, int64_t &smem) {
 }
 
 // The two-pass form: chunks of whole groups and whole vectors, about 512 bytes
-// wide, or pieces of a group wider than a block; slabs of pixels so that there
-// are about eight blocks of 256 threads for each of 148 SMs while a thread
-// still has eight pixels.  Returns the elements of a vector.
+// wide, or pieces of a group wider than a block; slabs of pixels so that all
+// blocks (three on each of 148 SMs) run at once, while a thread still has
+// eight pixels: a warp spends some 850 instructions on its place and its sums,
+// 24 on a vector.  Returns the elements of a vector.
 int plan_passes(GnParams &P, int vec, int32_t dtype) {
     int unit;   // groups that are whole vectors
     for (;; vec /= 2) {
@@ -184,7 +184,7 @@ int plan_passes(GnParams &P, int vec, int32_t dtype) {
     P.tx = P.width / vec;
     P.threads = kPassThreads;
     P.ty = P.threads / P.tx;
-    const int64_t want = std::max<int64_t>(1, 148 * 8 / std::max<int64_t>(1, int64_t(P.N) * P.chunks));
+    const int64_t want = std::max<int64_t>(1, 148 * 3 / std::max<int64_t>(1, int64_t(P.N) * P.chunks));
     const int64_t most = ceil_div(P.HW, int64_t(P.ty) * 8);
     P.slab = static_cast<int32_t>(ceil_div(P.HW, std::min(want, most)));
     P.slabs = static_cast<int32_t>(ceil_div(P.HW, P.slab));
@@ -202,6 +202,13 @@ struct GnPlan {
 GnPlan make_plan(GnParams &P, int vec, int32_t dtype, bool bwd) {
     GnPlan p{vec, false, 0, 0, 0};
     p.chip = plan_chip(P, vec, dtype, bwd, p.smem);
+    // Clusters of 16 CTAs with nearly all of their shared memory leave an SM
+    // nothing to overlap their phases with; once the tensors are large, two
+    // passes of many small blocks are faster, the second one partly out of L2:
+    // 16x64x160x160 bf16 39.8 against 44.1 us, backward 70.7 against 114; at
+    // 26 MB (4x64x160x160) 21.6 against 17.3.
+    const int64_t bytes = int64_t(P.N) * P.C * P.HW * dtype_bytes(dtype) * (bwd ? 3 : 2);
+    if (P.splits == 16 && bytes > (int64_t(32) << 20)) p.chip = false;
     if (p.chip) {
         P.slabs = 1;
         P.pieces = 1;
@@ -223,21 +230,23 @@ GnPlan make_plan(GnParams &P, int vec, int32_t dtype, bool bwd) {
     return p;
 }
 
-template <typename T, int VEC, bool UNI>
-mqc_status launch(GnParams &P, const GnPlan &plan, bool bwd, const DeviceLimits &d, cudaStream_t s) {
-    const int channel_blocks = bwd && (P.ggamma || P.gbeta) ? static_cast<int>(ceil_div(P.C, 32)) : 0;
+template <typename T, int VEC, bool UNI, bool BWD>
+mqc_status launch(GnParams &P, const GnPlan &plan, const DeviceLimits &d, cudaStream_t s) {
+    const int channel_blocks = BWD && (P.ggamma || P.gbeta) ? static_cast<int>(ceil_div(P.C, 32)) : 0;
     if constexpr (VEC * sizeof(T) >= 4)
         if (plan.chip) {
-            void (*kernel)(GnParams) = bwd ? gn_chip_bwd_kernel<T, VEC, UNI> : gn_chip_fwd_kernel<T, VEC, UNI>;
-            static std::atomic<bool> allowed[2][64];
-            if (!allowed[bwd][d.device].load(std::memory_order_acquire)) {
+            void (*kernel)(GnParams);
+            if constexpr (BWD) kernel = gn_chip_bwd_kernel<T, VEC, UNI>;
+            else kernel = gn_chip_fwd_kernel<T, VEC, UNI>;
+            static std::atomic<bool> allowed[64];
+            if (!allowed[d.device].load(std::memory_order_acquire)) {
                 cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, kChipSmem);
                 if (e == cudaSuccess)
                     e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
                 if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(group norm)");
-                allowed[bwd][d.device].store(true, std::memory_order_release);
+                allowed[d.device].store(true, std::memory_order_release);
             }
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(static_cast<unsigned>(int64_t(P.N) * P.chunks * P.splits));
@@ -262,7 +271,7 @@ mqc_status launch(GnParams &P, const GnPlan &plan, bool bwd, const DeviceLimits 
         }
     const unsigned grid = static_cast<unsigned>(int64_t(P.N) * P.slabs * P.chunks);
     const size_t nt = size_t(P.tx) * P.ty, groups = 2 * size_t(P.gpc) * 4;
-    if (bwd) {
+    if constexpr (BWD) {
         P.channel_blocks = channel_blocks;
         const size_t sums = 4 * (2 * nt * VEC + 2 * P.threads + 2 * size_t(P.tx) * VEC);
         const size_t join = P.threads / 32 * 2 * 32 * 8;
@@ -276,14 +285,18 @@ mqc_status launch(GnParams &P, const GnPlan &plan, bool bwd, const DeviceLimits 
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "group norm launch");
 }
 
-template <typename T>
-mqc_status launch_vec(GnParams &P, const GnPlan &plan, bool bwd, const DeviceLimits &d, cudaStream_t s) {
+template <typename T, bool BWD>
+mqc_status launch_vec(GnParams &P, const GnPlan &plan, const DeviceLimits &d, cudaStream_t s) {
     const bool uni = P.D % plan.vec == 0;   // always, with one channel a vector
-    if constexpr (sizeof(T) == 2)
-        if (plan.vec == 8) return uni ? launch<T, 8, true>(P, plan, bwd, d, s) : launch<T, 8, false>(P, plan, bwd, d, s);
-    if (plan.vec == 4) return uni ? launch<T, 4, true>(P, plan, bwd, d, s) : launch<T, 4, false>(P, plan, bwd, d, s);
-    if (plan.vec == 2) return uni ? launch<T, 2, true>(P, plan, bwd, d, s) : launch<T, 2, false>(P, plan, bwd, d, s);
-    return launch<T, 1, true>(P, plan, bwd, d, s);
+    if constexpr (sizeof(T) == 2 && !BWD)
+        if (plan.vec == 8) return uni ? launch<T, 8, true, BWD>(P, plan, d, s) : launch<T, 8, false, BWD>(P, plan, d, s);
+    if (plan.vec == 4) return uni ? launch<T, 4, true, BWD>(P, plan, d, s) : launch<T, 4, false, BWD>(P, plan, d, s);
+    if (plan.vec == 2) return uni ? launch<T, 2, true, BWD>(P, plan, d, s) : launch<T, 2, false, BWD>(P, plan, d, s);
+    return launch<T, 1, true, BWD>(P, plan, d, s);
+}
+template <typename T>
+mqc_status launch_dir(GnParams &P, const GnPlan &plan, bool bwd, const DeviceLimits &d, cudaStream_t s) {
+    return bwd ? launch_vec<T, true>(P, plan, d, s) : launch_vec<T, false>(P, plan, d, s);
 }
 
 mqc_status check_workspace(const char *name, const void *ws, size_t bytes, size_t need) {
@@ -301,9 +314,9 @@ mqc_status run(const char *name, GnParams &P, const GnPlan &plan, int32_t dtype,
     DeviceLimits d;
     mqc_status st = device_limits(&d);
     if (st != MQC_OK) return st;
-    if (dtype == MQC_F32) return launch_vec<float>(P, plan, bwd, d, s);
-    if (dtype == MQC_BF16) return launch_vec<__nv_bfloat16>(P, plan, bwd, d, s);
-    return launch_vec<__half>(P, plan, bwd, d, s);
+    if (dtype == MQC_F32) return launch_dir<float>(P, plan, bwd, d, s);
+    if (dtype == MQC_BF16) return launch_dir<__nv_bfloat16>(P, plan, bwd, d, s);
+    return launch_dir<__half>(P, plan, bwd, d, s);
 }
 
 void fill(GnParams &P, const mqc_t4 *d, int32_t groups) {

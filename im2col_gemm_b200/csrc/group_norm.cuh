@@ -332,25 +332,40 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_stats_kernel(const __grid_
     {
         const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
         const int64_t step = P.ty * P.x.sp;
-        constexpr int U = 8;
-        for (int i = 0; i < at.count; i += U) {
-            typename V::Raw r[U];
+        constexpr int U = 4;
+        int i = 0;
+        if (at.count > 0) {
+            float v[VEC];
+            V::widen(V::load(x), v);
+            run.start(v);
+        }
+        // the next batch is under way while one is summed
+        typename V::Raw r[U];
+        if (at.count >= U) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i + u < at.count) r[u] = V::load(x + u * step);
+            for (int u = 0; u < U; ++u) r[u] = V::load(x + u * step);
+        }
+#pragma unroll 2
+        for (; i + U <= at.count; i += U) {
+            typename V::Raw next[U];
             x += U * step;
-            if (i == 0) {
-                float v[VEC];
-                V::widen(r[0], v);
-                run.start(v);
+            if (i + 2 * U <= at.count) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) next[u] = V::load(x + u * step);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i + u < at.count) {
-                    float v[VEC];
-                    V::widen(r[u], v);
-                    run.add(v);
-                }
+            for (int u = 0; u < U; ++u) {
+                float v[VEC];
+                V::widen(r[u], v);
+                run.add(v);
+                r[u] = next[u];
+            }
+        }
+#pragma unroll 1
+        for (; i < at.count; ++i, x += step) {
+            float v[VEC];
+            V::widen(V::load(x), v);
+            run.add(v);
         }
     }
     run.finish(at.count);
@@ -402,11 +417,12 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_apply_kernel(const __grid_
     const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
     T *y = static_cast<T *>(P.out) + at.n * P.on + at.c + at.p0 * P.op;
     const int64_t xstep = P.ty * P.x.sp, ystep = P.ty * P.op;
-    constexpr int U = 4;
+    constexpr int U = 2;
     typename V::Raw r[U];
+    if (at.count >= U) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (u < at.count) r[u] = V::load(x + u * xstep);
+        for (int u = 0; u < U; ++u) r[u] = V::load(x + u * xstep);
+    }
     float a[VEC], b[VEC], m[VEC];
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {
@@ -435,25 +451,32 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_apply_kernel(const __grid_
         m[q] = -mean[g];
         a[q] *= rstd[g];
     });
-    for (int i = 0; i < at.count; i += U) {
-        if (i > 0) {
+    auto one = [&](const typename V::Raw &raw, T *to) {
+        float v[VEC];
+        V::widen(raw, v);
+        add_to(v, m);
+        fma_to(v, v, a, b);
+        act_values<true>(P.act, v);
+        V::store(to, v);
+    };
+    int i = 0;
+#pragma unroll 2
+    for (; i + U <= at.count; i += U) {
+        typename V::Raw next[U];
+        x += U * xstep;
+        if (i + 2 * U <= at.count) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i + u < at.count) r[u] = V::load(x + u * xstep);
+            for (int u = 0; u < U; ++u) next[u] = V::load(x + u * xstep);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i + u < at.count) {
-                float v[VEC];
-                V::widen(r[u], v);
-                add_to(v, m);
-                fma_to(v, v, a, b);
-                act_values<true>(P.act, v);
-                V::store(y + u * ystep, v);
-            }
-        x += U * xstep;
+        for (int u = 0; u < U; ++u) {
+            one(r[u], y + u * ystep);
+            r[u] = next[u];
+        }
         y += U * ystep;
     }
+#pragma unroll 1
+    for (; i < at.count; ++i, x += xstep, y += ystep) one(V::load(x), y);
 }
 
 // What the backward pass keeps of a thread's channels.
@@ -495,28 +518,44 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_sums_kernel(const __gr
         const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
         const T *g = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c + at.p0 * P.g.sp;
         const int64_t xstep = P.ty * P.x.sp, gstep = P.ty * P.g.sp;
-        constexpr int U = 4;
-        for (int i = 0; i < at.count; i += U) {
-            typename V::Raw rx[U], rg[U];
+        constexpr int U = 2;
+        auto one = [&](const typename V::Raw &rx, const typename V::Raw &rg) {
+            float xv[VEC], gv[VEC];
+            V::widen(rx, xv);
+            V::widen(rg, gv);
+            K.apply(P.act, xv, gv);
+            add_to(sa, gv);
+            fma_to(sb, gv, xv, sb);
+        };
+        int i = 0;
+        typename V::Raw rx[U], rg[U];
+        if (at.count >= U) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i + u < at.count) {
-                    rx[u] = V::load(x + u * xstep);
-                    rg[u] = V::load(g + u * gstep);
-                }
+            for (int u = 0; u < U; ++u) {
+                rx[u] = V::load(x + u * xstep);
+                rg[u] = V::load(g + u * gstep);
+            }
+        }
+#pragma unroll 2
+        for (; i + U <= at.count; i += U) {
+            typename V::Raw nx[U], ng[U];
             x += U * xstep;
             g += U * gstep;
+            if (i + 2 * U <= at.count) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i + u < at.count) {
-                    float xv[VEC], gv[VEC];
-                    V::widen(rx[u], xv);
-                    V::widen(rg[u], gv);
-                    K.apply(P.act, xv, gv);
-                    add_to(sa, gv);
-                    fma_to(sb, gv, xv, sb);
+                for (int u = 0; u < U; ++u) {
+                    nx[u] = V::load(x + u * xstep);
+                    ng[u] = V::load(g + u * gstep);
                 }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                one(rx[u], rg[u]);
+                rx[u] = nx[u];
+                rg[u] = ng[u];
+            }
         }
+        if (i < at.count) one(V::load(x), V::load(g));
     }
     const int nt = P.tx * P.ty, cb = P.tx * VEC, c0 = at.c - at.col * VEC;
     float *part = gn_red + 2 * nt * VEC, *csum = part + 2 * blockDim.x;
@@ -551,12 +590,13 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_apply_kernel(const __g
     const int64_t xstep = P.ty * P.x.sp, gstep = P.ty * P.g.sp, ostep = P.ty * P.op;
     constexpr int U = 2;
     typename V::Raw rx[U], rg[U];
+    if (at.count >= U) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-        if (u < at.count) {
+        for (int u = 0; u < U; ++u) {
             rx[u] = V::load(x + u * xstep);
             rg[u] = V::load(g + u * gstep);
         }
+    }
     GnSlope<VEC> K;
     K.template load<UNI>(P, at.n, group0, at.col * VEC, at.c, at.on);
     for (int j = threadIdx.x / 32; j < P.gpc; j += blockDim.x / 32) {
@@ -580,30 +620,32 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_apply_kernel(const __g
         c1[q] = -K.rstd[q] * k1[j];
         c2[q] = -K.rstd[q] * k2[j];
     });
-    for (int i = 0; i < at.count; i += U) {
+    auto one = [&](const typename V::Raw &rx, const typename V::Raw &rg, T *to) {
+        float xv[VEC], gv[VEC];
+        V::widen(rx, xv);
+        V::widen(rg, gv);
+        K.apply(P.act, xv, gv);
+        fma_to(xv, xv, c2, c1);
+        fma_to(gv, gv, scale, xv);
+        V::store(to, gv);
+    };
+    int i = 0;
+    // (no second batch under way here: its registers would spill)
+    for (; i + U <= at.count; i += U) {
         if (i > 0) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i + u < at.count) {
-                    rx[u] = V::load(x + u * xstep);
-                    rg[u] = V::load(g + u * gstep);
-                }
+            for (int u = 0; u < U; ++u) {
+                rx[u] = V::load(x + u * xstep);
+                rg[u] = V::load(g + u * gstep);
+            }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (i + u < at.count) {
-                float xv[VEC], gv[VEC];
-                V::widen(rx[u], xv);
-                V::widen(rg[u], gv);
-                K.apply(P.act, xv, gv);
-                fma_to(xv, xv, c2, c1);
-                fma_to(gv, gv, scale, xv);
-                V::store(o + u * ostep, gv);
-            }
+        for (int u = 0; u < U; ++u) one(rx[u], rg[u], o + u * ostep);
         x += U * xstep;
         g += U * gstep;
         o += U * ostep;
     }
+    if (i < at.count) one(V::load(x), V::load(g), o);
 }
 
 // ---------------------------------------------------------------- one pass
