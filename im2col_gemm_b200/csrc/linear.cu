@@ -46,73 +46,24 @@ mqc_status allow_smem(const void *kernel, int index, const DeviceLimits &d) {
 
 // D[token][feature] = sum over `red` of X . W: X indexed by token, W by
 // feature; the epilogue stores rows of tokens.
-mqc_status launch_product(Operand X, Operand W, int32_t tokens, int32_t features, int32_t red, int32_t dtype,
-                          const Epilogue &E, const DeviceLimits &d, cudaStream_t stream) {
-    LinParams P;
-    const bool bf16 = dtype == MQC_BF16;
+struct Product {
+    Operand X, W;
+    int32_t tokens, features, red;
+    Epilogue E;
     // few tokens: the features fill the 128 rows of the tensor core's tile
     // and the tokens its columns, so that no rows are spent on padding
-    P.swap = tokens <= 64;
-    const Operand &A = P.swap ? W : X, &B = P.swap ? X : W;
-    P.I = P.swap ? features : tokens;
-    P.J = P.swap ? tokens : features;
-    P.R = red;
+    bool swap() const { return tokens <= 64; }
+    int64_t kblocks() const { return ceil_div(red, kLinBK); }
+};
+
+// What both kernels need besides the tiling; `a_rows`, `b_rows`: box rows.
+mqc_status fill_params(LinParams &P, const Product &p, bool bf16, int rows, bool pair) {
+    const Operand &A = P.swap ? p.W : p.X, &B = P.swap ? p.X : p.W;
+    const Epilogue &E = p.E;
+    P.R = p.red;
     P.a_mn = A.mn;
     P.b_mn = B.mn;
-    P.splits = 1;
-    const int nkb = static_cast<int>(ceil_div(red, kLinBK));
-    const int room = d.max_smem - 2048 - 1024;
-    int64_t grid;
-    int cluster, threads, smem, a_rows, b_rows;
-    // CTA pairs once their 256-row tiles fill most of the SM pairs
-    const int64_t pair_rows = ceil_div(P.I, 2 * kLinRows);
-    const int pairs = d.sms / 2;
-    const bool pair = !P.swap && pair_rows * ceil_div(P.J, 128) >= pairs * 3 / 4;
-    if (pair) {
-        // 256 or 128 columns: the fewer rounds of tiles, a narrow tile counted
-        // as 0.6 of a wide one
-        const int64_t wide = ceil_div(pair_rows * ceil_div(P.J, 256), pairs) * 10;
-        const int64_t narrow = ceil_div(pair_rows * ceil_div(P.J, 128), pairs) * 6;
-        P.bn = narrow < wide ? 128 : 256;
-        P.tiles_i = static_cast<int32_t>(pair_rows);
-        P.b_bytes = P.bn / 2 * kLinBK * 2;
-        const int64_t tiles = pair_rows * ceil_div(P.J, P.bn);
-        const int stage = kLinRows * kLinBK * 2 + P.b_bytes;
-        P.stages = std::min(kPairMaxStages, (room - kPairStaging) / stage);
-        smem = 1024 + P.stages * stage + kPairStaging;
-        grid = 2 * std::min<int64_t>(tiles, pairs);
-        if (tiles > (int64_t(1) << 30)) return fail(MQC_ERR_INVALID, "linear: too many tiles");
-        P.idesc = make_idesc_f16(bf16, P.a_mn, P.b_mn, 2 * kLinRows, P.bn);
-        cluster = 2;
-        threads = kPairThreads;
-        a_rows = kLinRows;
-        b_rows = P.bn / 2;
-    } else {
-        P.tiles_i = static_cast<int32_t>(ceil_div(P.I, kLinRows));
-        // the widest column tile that still gives every SM one; all the tokens
-        // of the swapped form in one tile, so that the weights are read once
-        if (P.swap) {
-            P.bn = static_cast<int32_t>(round_up(P.J, 16));
-        } else {
-            P.bn = 256;
-            while (P.bn > 32 && (P.bn / 2 >= P.J || P.tiles_i * ceil_div(P.J, P.bn) < d.sms)) P.bn /= 2;
-        }
-        const int64_t tiles = P.tiles_i * ceil_div(P.J, P.bn);
-        while (P.splits < 8 && tiles * P.splits < d.sms && nkb / (2 * P.splits) >= 2) P.splits *= 2;
-        P.b_bytes = (P.b_mn ? static_cast<int>(round_up(P.bn, 64)) : P.bn) * kLinBK * 2;
-        const int stage = kLinRows * kLinBK * 2 + P.b_bytes;
-        const int part = P.swap ? P.bn * kLinRows * 4 : kLinRows * (P.bn + 1) * 4;
-        const int share = tiles * P.splits > d.sms && P.bn <= 64 ? room / 2 - 512 : room;
-        P.stages = std::max(1, std::min({kLinMaxStages, share / stage, static_cast<int>(ceil_div(nkb, P.splits))}));
-        smem = 1024 + std::max(P.stages * stage, part);
-        grid = tiles * P.splits;
-        if (grid > (int64_t(1) << 31) - 1) return fail(MQC_ERR_INVALID, "linear: too many tiles");
-        P.idesc = make_idesc_f16(bf16, P.a_mn, P.b_mn, kLinRows, P.bn);
-        cluster = P.splits;
-        threads = kLinThreads;
-        a_rows = kLinRows;
-        b_rows = P.bn;
-    }
+    P.idesc = make_idesc_f16(bf16, A.mn, B.mn, rows, P.bn);
     P.tma_out = pair && E.ldy % 8 == 0 && (!E.z || E.ldz % 8 == 0) && (!E.res || E.ldr % 8 == 0);
     P.act = E.act;
     P.bias = E.bias;
@@ -122,20 +73,23 @@ mqc_status launch_product(Operand X, Operand W, int32_t tokens, int32_t features
     P.ldr = E.ldr;
     P.ldy = E.ldy;
     P.ldz = E.ldz;
-    mqc_status st = A.mn ? encode_matrix_map(&P.amap, A.p, red, P.I, A.ld, kLinBK)
-                         : encode_matrix_map(&P.amap, A.p, P.I, red, A.ld, a_rows);
+    mqc_status st = A.mn ? encode_matrix_map(&P.amap, A.p, p.red, P.I, A.ld, kLinBK)
+                         : encode_matrix_map(&P.amap, A.p, P.I, p.red, A.ld, kLinRows);
     if (st != MQC_OK) return st;
-    st = B.mn ? encode_matrix_map(&P.bmap, B.p, red, P.J, B.ld, kLinBK)
-              : encode_matrix_map(&P.bmap, B.p, P.J, red, B.ld, b_rows);
+    st = B.mn ? encode_matrix_map(&P.bmap, B.p, p.red, P.J, B.ld, kLinBK)
+              : encode_matrix_map(&P.bmap, B.p, P.J, p.red, B.ld, pair ? P.bn / 2 : P.bn);
+    if (st == MQC_OK && P.tma_out) st = encode_matrix_map(&P.ymap, E.y, P.I, P.J, E.ldy, 32, 64);
+    if (st == MQC_OK && P.tma_out && E.z) st = encode_matrix_map(&P.zmap, E.z, P.I, P.J, E.ldz, 32, 64);
+    return st;
+}
+
+mqc_status launch_group(const LinGroup &G, bool pair, bool bf16, int64_t grid, int cluster, int threads, int smem,
+                        const DeviceLimits &d, cudaStream_t stream) {
+    if (grid > (int64_t(1) << 31) - 1) return fail(MQC_ERR_INVALID, "linear: too many tiles");
+    void (*kernel)(LinGroup) = pair ? (bf16 ? linear_pair_kernel<__nv_bfloat16> : linear_pair_kernel<__half>)
+                                    : (bf16 ? linear_tile_kernel<__nv_bfloat16> : linear_tile_kernel<__half>);
+    mqc_status st = allow_smem(reinterpret_cast<const void *>(kernel), 2 * pair + bf16, d);
     if (st != MQC_OK) return st;
-    if (P.tma_out) {
-        st = encode_matrix_map(&P.ymap, E.y, P.I, P.J, E.ldy, 32, 64);
-        if (st == MQC_OK && E.z) st = encode_matrix_map(&P.zmap, E.z, P.I, P.J, E.ldz, 32, 64);
-        if (st != MQC_OK) return st;
-    }
-    void (*kernel)(LinParams) = pair ? (bf16 ? linear_pair_kernel<__nv_bfloat16> : linear_pair_kernel<__half>)
-                                     : (bf16 ? linear_tile_kernel<__nv_bfloat16> : linear_tile_kernel<__half>);
-    if ((st = allow_smem(reinterpret_cast<const void *>(kernel), 2 * pair + bf16, d)) != MQC_OK) return st;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(threads);
@@ -148,8 +102,121 @@ mqc_status launch_product(Operand X, Operand W, int32_t tokens, int32_t features
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, G);
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear kernel launch");
+}
+
+// One or two products on CTA pairs, the longer reduction's tiles first (they
+// are dealt out in turn, so the shorter ones even out the end).
+mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool bf16, const DeviceLimits &d,
+                        cudaStream_t stream) {
+    const int pairs = d.sms / 2;
+    const Product *order[2] = {&p[0], count > 1 ? &p[1] : nullptr};
+    if (count > 1 && p[1].kblocks() > p[0].kblocks()) std::swap(order[0], order[1]);
+    // 256 or 128 columns: the shorter way for the busiest pair, a narrow tile
+    // counted as 0.6 of a wide one
+    auto tiles_of = [](const Product &q, int bn) { return ceil_div(q.tokens, 2 * kLinRows) * ceil_div(q.features, bn); };
+    auto busiest = [&](int bn) {
+        const int64_t t0 = tiles_of(*order[0], bn), t1 = count > 1 ? tiles_of(*order[1], bn) : 0;
+        int64_t most = 0;
+        for (int c = 0; c < pairs; ++c) {
+            const int64_t n0 = (t0 - c + pairs - 1) / pairs, n = (t0 + t1 - c + pairs - 1) / pairs;
+            most = std::max(most, n0 * order[0]->kblocks() + (count > 1 ? (n - n0) * order[1]->kblocks() : 0));
+        }
+        return most;
+    };
+    const int bn = busiest(128) * 6 < busiest(256) * 10 ? 128 : 256;
+    const int b_bytes = bn / 2 * kLinBK * 2, stage = kLinRows * kLinBK * 2 + b_bytes;
+    const int stages = std::min(kPairMaxStages, (d.max_smem - 2048 - 1024 - kPairStaging) / stage);
+    LinGroup G{};
+    G.bias = bias;
+    int64_t tiles = 0;
+    for (int i = 0; i < count; ++i) {
+        LinParams &P = G.p[i];
+        P.I = order[i]->tokens;
+        P.J = order[i]->features;
+        P.bn = bn;
+        P.b_bytes = b_bytes;
+        P.stages = stages;
+        P.splits = 1;
+        P.tiles_i = static_cast<int32_t>(ceil_div(P.I, 2 * kLinRows));
+        tiles += tiles_of(*order[i], bn);
+        if (tiles > (int64_t(1) << 30)) return fail(MQC_ERR_INVALID, "linear: too many tiles");
+        if (i == 0) G.first = static_cast<int32_t>(tiles);
+        mqc_status st = fill_params(P, *order[i], bf16, 2 * kLinRows, true);
+        if (st != MQC_OK) return st;
+    }
+    G.tiles = static_cast<int32_t>(tiles);
+    return launch_group(G, true, bf16, 2 * std::min<int64_t>(tiles, pairs), 2, kPairThreads,
+                        1024 + stages * stage + kPairStaging, d, stream);
+}
+
+// One or two products on single tiles.  A product's plan does not depend on
+// the other's presence, nor then do its bits.
+mqc_status launch_tiles(const Product *p, int count, const BiasGrad &bias, bool bf16, const DeviceLimits &d,
+                        cudaStream_t stream) {
+    LinGroup G{};
+    G.bias = bias;
+    G.cluster = 1;
+    int64_t ctas = 0;
+    for (int i = 0; i < count; ++i) {
+        LinParams &P = G.p[i];
+        P.swap = p[i].swap();
+        P.I = P.swap ? p[i].features : p[i].tokens;
+        P.J = P.swap ? p[i].tokens : p[i].features;
+        P.tiles_i = static_cast<int32_t>(ceil_div(P.I, kLinRows));
+        // the widest column tile that still gives every SM one; all the tokens
+        // of the swapped form in one tile, so that the weights are read once
+        if (P.swap) {
+            P.bn = static_cast<int32_t>(round_up(P.J, 16));
+        } else {
+            P.bn = 256;
+            while (P.bn > 32 && (P.bn / 2 >= P.J || P.tiles_i * ceil_div(P.J, P.bn) < d.sms)) P.bn /= 2;
+        }
+        const int64_t tiles = P.tiles_i * ceil_div(P.J, P.bn);
+        if (tiles > (int64_t(1) << 30) / 16) return fail(MQC_ERR_INVALID, "linear: too many tiles");
+        P.tiles = static_cast<int32_t>(tiles);
+        P.splits = 1;
+        while (P.splits < 8 && tiles * P.splits < d.sms && p[i].kblocks() / (2 * P.splits) >= 2) P.splits *= 2;
+        G.cluster = std::max(G.cluster, P.splits);
+        ctas += tiles * P.splits;
+    }
+    int smem = 0;
+    for (int i = 0; i < count; ++i) {
+        LinParams &P = G.p[i];
+        const bool b_mn = P.swap ? p[i].X.mn : p[i].W.mn;
+        P.b_bytes = (b_mn ? static_cast<int>(round_up(P.bn, 64)) : P.bn) * kLinBK * 2;
+        const int stage = kLinRows * kLinBK * 2 + P.b_bytes;
+        const int part = P.swap ? P.bn * kLinRows * 4 : kLinRows * (P.bn + 1) * 4;
+        const int room = d.max_smem - 2048 - 1024;
+        const int share = ctas > d.sms && P.bn <= 64 ? room / 2 - 512 : room;
+        P.stages = std::max(1, std::min({kLinMaxStages, share / stage,
+                                         static_cast<int>(ceil_div(p[i].kblocks(), P.splits))}));
+        smem = std::max(smem, 1024 + std::max(P.stages * stage, part));
+        G.tiles += static_cast<int32_t>(ceil_div(P.tiles, G.cluster / P.splits));   // clusters
+        if (i == 0) G.first = G.tiles;
+        mqc_status st = fill_params(P, p[i], bf16, kLinRows, false);
+        if (st != MQC_OK) return st;
+    }
+    const int64_t extra = bias.gb ? round_up(ceil_div(bias.N, kLinThreads), G.cluster) : 0;
+    return launch_group(G, false, bf16, int64_t(G.tiles) * G.cluster + extra, G.cluster, kLinThreads, smem, d, stream);
+}
+
+// The products of a call, and its bias gradient's last sums beside them: in
+// one launch when the same kernel suits them.  CTA pairs once their 256-row
+// tiles fill most of the SM pairs.
+mqc_status launch_products(const Product *p, int count, const BiasGrad &bias, int32_t dtype, const DeviceLimits &d,
+                           cudaStream_t stream) {
+    const bool bf16 = dtype == MQC_BF16;
+    int64_t narrow = 0;
+    for (int i = 0; i < count; ++i)
+        narrow += p[i].swap() ? 0 : ceil_div(p[i].tokens, 2 * kLinRows) * ceil_div(p[i].features, 128);
+    const bool enough = narrow >= d.sms / 2 * 3 / 4;
+    if (count > 1 && p[0].swap() != p[1].swap()) {
+        mqc_status st = launch_products(p, 1, bias, dtype, d, stream);
+        return st != MQC_OK ? st : launch_products(p + 1, 1, BiasGrad{}, dtype, d, stream);
+    }
+    return enough ? launch_pairs(p, count, bias, bf16, d, stream) : launch_tiles(p, count, bias, bf16, d, stream);
 }
 
 // Bytes of a padded copy of a rows x cols matrix, and whether one is needed.
@@ -158,19 +225,55 @@ size_t packed_bytes(int64_t rows, int64_t cols) {
     return static_cast<size_t>(round_up(rows * round_up(cols, 8) * 2, 256));
 }
 
-mqc_status pack(Operand &op, int64_t rows, int64_t cols, uint8_t *&ws, cudaStream_t stream, const DeviceLimits &d) {
-    if (!needs_pack(op.ld)) return MQC_OK;
-    const int64_t ldd = round_up(cols, 8);
-    const int64_t blocks = std::min<int64_t>(ceil_div(rows * (ldd / 8), 256), int64_t(d.sms) * 8);
-    linear_pack_kernel<<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-        static_cast<const uint16_t *>(op.p), op.ld, rows, static_cast<int32_t>(cols), reinterpret_cast<uint16_t *>(ws),
-        ldd);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return cuda_fail(e, "linear_pack_kernel launch");
+// Plans the copy of an operand, if its rows need one, into the workspace at ws.
+void plan_pack(PackJob &job, Operand &op, int64_t rows, int64_t cols, uint8_t *&ws, const DeviceLimits &d) {
+    if (!needs_pack(op.ld)) return;
+    job.src = static_cast<const uint16_t *>(op.p);
+    job.dst = reinterpret_cast<uint16_t *>(ws);
+    job.ld = op.ld;
+    job.rows = rows;
+    job.cols = static_cast<int32_t>(cols);
+    job.ldd = round_up(cols, 8);
+    job.blocks = static_cast<int32_t>(std::min<int64_t>(ceil_div(rows * (job.ldd / 8), 256), int64_t(d.sms) * 8));
     op.p = ws;
-    op.ld = ldd;
+    op.ld = job.ldd;
     ws += packed_bytes(rows, cols);
-    return MQC_OK;
+}
+
+mqc_status launch_prep(const LinPrep &prep, int32_t dtype, cudaStream_t stream) {
+    const int64_t blocks = int64_t(prep.dz.blocks) + prep.pack[0].blocks + prep.pack[1].blocks;
+    if (blocks == 0) return MQC_OK;
+    if (blocks > (int64_t(1) << 31) - 1) return fail(MQC_ERR_INVALID, "linear: too many blocks");
+    const bool vec = prep.dz.ldg % 8 == 0 && (prep.dz.z == nullptr || prep.dz.ldz % 8 == 0);
+    const unsigned grid = static_cast<unsigned>(blocks);
+    if (dtype == MQC_BF16) {
+        if (vec) linear_prep_kernel<__nv_bfloat16, true><<<grid, 256, 0, stream>>>(prep);
+        else linear_prep_kernel<__nv_bfloat16, false><<<grid, 256, 0, stream>>>(prep);
+    } else {
+        if (vec) linear_prep_kernel<__half, true><<<grid, 256, 0, stream>>>(prep);
+        else linear_prep_kernel<__half, false><<<grid, 256, 0, stream>>>(prep);
+    }
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear_prep_kernel launch");
+}
+
+// One to eight tokens (linear_few_kernel).  Four features a block (two beyond
+// two tokens, for the registers) where that still leaves a block or more an
+// SM several times over, else one.
+constexpr int kFewTokens = 8;
+template <typename T, int MT, int RN>
+void launch_few_as(const LinFew &P, bool vec, cudaStream_t s) {
+    const unsigned grid = static_cast<unsigned>(ceil_div(P.N, RN));
+    if (vec) linear_few_kernel<T, MT, RN, true><<<grid, 256, 0, s>>>(P);
+    else linear_few_kernel<T, MT, RN, false><<<grid, 256, 0, s>>>(P);
+}
+template <typename T>
+void launch_few(const LinFew &P, cudaStream_t s) {
+    const bool vec = P.ldw % 8 == 0 && (P.M == 1 || P.ldx % 8 == 0), wide = P.N >= 2048;
+    if (P.M == 1) wide ? launch_few_as<T, 1, 4>(P, vec, s) : launch_few_as<T, 1, 1>(P, vec, s);
+    else if (P.M == 2) wide ? launch_few_as<T, 2, 4>(P, vec, s) : launch_few_as<T, 2, 1>(P, vec, s);
+    else if (P.M <= 4) wide ? launch_few_as<T, 4, 2>(P, vec, s) : launch_few_as<T, 4, 1>(P, vec, s);
+    else wide ? launch_few_as<T, 8, 2>(P, vec, s) : launch_few_as<T, 8, 1>(P, vec, s);
 }
 
 mqc_status check_linear(const mqc_linear *l, const char *name) {
@@ -210,20 +313,6 @@ void dz_slabs(int64_t M, int64_t N, int32_t &slab, int32_t &slabs) {
     slabs = static_cast<int32_t>(ceil_div(M, slab));
 }
 
-template <typename T>
-void launch_dz(const mqc_linear *l, const void *g, const void *z, void *dz, float *part, int32_t slab, int32_t slabs,
-               cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(ceil_div(l->N, 256)), static_cast<unsigned>(slabs));
-    const T *gp = static_cast<const T *>(g), *zp = static_cast<const T *>(z);
-    const int64_t lddz = round_up(l->N, 8);
-    if (l->ldg % 8 == 0 && (z == nullptr || l->ldz % 8 == 0))
-        linear_dz_kernel<T, true><<<grid, 256, 0, stream>>>(gp, l->ldg, zp, l->ldz, l->M, l->N, l->act,
-                                                            static_cast<T *>(dz), lddz, part, slab);
-    else
-        linear_dz_kernel<T, false><<<grid, 256, 0, stream>>>(gp, l->ldg, zp, l->ldz, l->M, l->N, l->act,
-                                                             static_cast<T *>(dz), lddz, part, slab);
-}
-
 }  // namespace
 }  // namespace mqc
 
@@ -232,7 +321,7 @@ using namespace mqc;
 extern "C" {
 
 size_t mqc_linear_fwd_workspace_bytes(const mqc_linear *l) {
-    if (check_linear(l, "linear_fwd") != MQC_OK) return 0;
+    if (check_linear(l, "linear_fwd") != MQC_OK || l->M <= kFewTokens) return 0;
     return (needs_pack(l->ldx) ? packed_bytes(l->M, l->K) : 0) + (needs_pack(l->ldw) ? packed_bytes(l->N, l->K) : 0);
 }
 
@@ -253,20 +342,28 @@ mqc_status mqc_linear_fwd(const mqc_linear *l, const void *x, const void *w, con
     DeviceLimits d;
     if ((st = device_limits(&d)) != MQC_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (l->M <= kFewTokens) {
+        LinFew P{x, w, bias, residual, y, z, l->ldx, l->ldw, l->ldr, l->ldy, l->ldz, l->M, l->N, l->K, l->act};
+        if (l->dtype == MQC_BF16) launch_few<__nv_bfloat16>(P, s);
+        else launch_few<__half>(P, s);
+        cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear_few_kernel launch");
+    }
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    Operand X{x, l->ldx, false}, W{w, l->ldw, false};
-    if ((st = pack(X, l->M, l->K, ws, s, d)) != MQC_OK) return st;
-    if ((st = pack(W, l->N, l->K, ws, s, d)) != MQC_OK) return st;
-    Epilogue E;
-    E.bias = bias;
-    E.res = residual;
-    E.y = y;
-    E.z = z;
-    E.ldr = l->ldr;
-    E.ldy = l->ldy;
-    E.ldz = l->ldz;
-    E.act = l->act;
-    return launch_product(X, W, l->M, l->N, l->K, l->dtype, E, d, s);
+    Product p{{x, l->ldx, false}, {w, l->ldw, false}, l->M, l->N, l->K, {}};
+    LinPrep prep{};
+    plan_pack(prep.pack[0], p.X, l->M, l->K, ws, d);
+    plan_pack(prep.pack[1], p.W, l->N, l->K, ws, d);
+    if ((st = launch_prep(prep, l->dtype, s)) != MQC_OK) return st;
+    p.E.bias = bias;
+    p.E.res = residual;
+    p.E.y = y;
+    p.E.z = z;
+    p.E.ldr = l->ldr;
+    p.E.ldy = l->ldy;
+    p.E.ldz = l->ldz;
+    p.E.act = l->act;
+    return launch_products(&p, 1, BiasGrad{}, l->dtype, d, s);
 }
 
 size_t mqc_linear_bwd_workspace_bytes(const mqc_linear *l) {
@@ -308,46 +405,54 @@ mqc_status mqc_linear_bwd(const mqc_linear *l, const void *g, const void *z, con
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     int32_t slab, slabs;
     dz_slabs(l->M, l->N, slab, slabs);
-    float *part = gb ? reinterpret_cast<float *>(ws) : nullptr;
+    BiasGrad bias{gb ? reinterpret_cast<float *>(ws) : nullptr, gb, slabs, l->N};
     ws += round_up(int64_t(slabs) * l->N * 4, 256);
+    LinPrep prep{};
     Operand DZ{g, l->ldg, false};
-    void *dz = nullptr;
-    if ((gx || gw) && (act || needs_pack(l->ldg))) {
-        dz = ws;
-        DZ.p = dz;
-        DZ.ld = round_up(l->N, 8);
+    const bool copy = act || needs_pack(l->ldg);   // dz is not g as it stands
+    if (gb || copy) {
+        DzJob &J = prep.dz;
+        J.g = g;
+        J.z = act ? z : nullptr;
+        J.part = gb ? reinterpret_cast<float *>(workspace) : nullptr;
+        J.ldg = l->ldg;
+        J.ldz = l->ldz;
+        J.lddz = round_up(l->N, 8);
+        J.M = l->M;
+        J.N = l->N;
+        J.act = l->act;
+        J.slab = slab;
+        J.col_blocks = static_cast<int32_t>(ceil_div(l->N, 256));
+        if (int64_t(J.col_blocks) * slabs > (int64_t(1) << 30)) return fail(MQC_ERR_INVALID, "%s: too many blocks", name);
+        J.blocks = J.col_blocks * slabs;
+        if (copy && (gx || gw)) {
+            J.dz = ws;
+            DZ.p = ws;
+            DZ.ld = J.lddz;
+        }
+        if (copy) ws += packed_bytes(l->M, l->N);
     }
-    if (act || needs_pack(l->ldg)) ws += packed_bytes(l->M, l->N);
-    if (dz || part) {
-        if (l->dtype == MQC_BF16) launch_dz<__nv_bfloat16>(l, g, act ? z : nullptr, dz, part, slab, slabs, s);
-        else launch_dz<__half>(l, g, act ? z : nullptr, dz, part, slab, slabs, s);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return cuda_fail(e, "linear_dz_kernel launch");
-    }
-    if (part) {
-        linear_bias_grad_kernel<<<static_cast<unsigned>(ceil_div(l->N, 128)), 128, 0, s>>>(part, slabs, l->N, gb);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return cuda_fail(e, "linear_bias_grad_kernel launch");
-    }
+    Product p[2];
+    int count = 0;
     if (gx) {
-        Operand W{w, l->ldw, true};
-        if ((st = pack(W, l->N, l->K, ws, s, d)) != MQC_OK) return st;
-        Epilogue E;
-        E.y = gx;
-        E.ldy = l->ldgx;
-        if ((st = launch_product(DZ, W, l->M, l->K, l->N, l->dtype, E, d, s)) != MQC_OK) return st;
+        p[count] = Product{DZ, {w, l->ldw, true}, l->M, l->K, l->N, {}};
+        plan_pack(prep.pack[0], p[count].W, l->N, l->K, ws, d);
+        p[count].E.y = gx;
+        p[count++].E.ldy = l->ldgx;
     }
     if (gw) {
-        Operand X{x, l->ldx, true};
-        if ((st = pack(X, l->M, l->K, ws, s, d)) != MQC_OK) return st;
         Operand G = DZ;
         G.mn = true;
-        Epilogue E;
-        E.y = gw;
-        E.ldy = l->ldgw;
-        if ((st = launch_product(G, X, l->N, l->K, l->M, l->dtype, E, d, s)) != MQC_OK) return st;
+        p[count] = Product{G, {x, l->ldx, true}, l->N, l->K, l->M, {}};
+        plan_pack(prep.pack[1], p[count].W, l->M, l->K, ws, d);
+        p[count].E.y = gw;
+        p[count++].E.ldy = l->ldgw;
     }
-    return MQC_OK;
+    if ((st = launch_prep(prep, l->dtype, s)) != MQC_OK) return st;
+    if (count > 0) return launch_products(p, count, bias, l->dtype, d, s);
+    linear_bias_grad_kernel<<<static_cast<unsigned>(ceil_div(l->N, 128)), 128, 0, s>>>(bias);
+    cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear_bias_grad_kernel launch");
 }
 
 }  // extern "C"

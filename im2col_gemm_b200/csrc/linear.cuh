@@ -31,7 +31,7 @@ struct LinParams {
     int32_t a_mn, b_mn;              // operand stored with its own index innermost
     int32_t swap;                    // i is the feature and j the token (else i the token)
     int32_t bn;                      // rows of B per tile, a multiple of 16
-    int32_t tiles_i, splits, stages;
+    int32_t tiles_i, tiles, splits, stages;
     int32_t b_bytes;                 // bytes of B per stage
     uint32_t idesc;
     int32_t act;
@@ -41,6 +41,34 @@ struct LinParams {
     void *y, *z;
     int64_t ldr, ldy, ldz;
 };
+
+// The sums of a layer's bias gradient: gb[n] = sum of `slabs` partial rows.
+struct BiasGrad {
+    const float *part;
+    float *gb;
+    int32_t slabs, N;
+};
+
+// One launch: one or two products (of the same tile width where CTA pairs run
+// them) and a bias gradient's last sums.
+struct LinGroup {
+    LinParams p[2];
+    int32_t first;                   // tiles (single tiles: clusters) of p[0]; those of p[1] follow
+    int32_t tiles;                   // of both
+    int32_t cluster;                 // single tiles: CTAs of a cluster, a multiple of both products' splits
+    BiasGrad bias;                   // gb NULL: none
+};
+
+// One column's partial rows, in row order over four running sums.
+__device__ __forceinline__ void bias_grad_column(const BiasGrad &b, int c) {
+    float s[4] = {};
+    int k = 0;
+    for (; k + 4 <= b.slabs; k += 4)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s[q] += b.part[static_cast<int64_t>(k + q) * b.N + c];
+    for (; k < b.slabs; ++k) s[0] += b.part[static_cast<int64_t>(k) * b.N + c];
+    b.gb[c] = (s[0] + s[1]) + (s[2] + s[3]);
+}
 
 // Instruction descriptor of kind::f16 with fp32 accumulators (bit 4): operand
 // formats at bits 7 and 10 (0 = fp16, 1 = bf16), MN-major A at bit 15 and B at
@@ -87,9 +115,18 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
     return v;
 }
 
+struct LinFew {
+    const void *x, *w;
+    const float *bias;
+    const void *res;
+    void *y, *z;
+    int64_t ldx, ldw, ldr, ldy, ldz;
+    int32_t M, N, K, act;
+};
+
 // bias, activation and residual of one element, z and y stored.
-template <typename T>
-__device__ __forceinline__ void lin_store(const LinParams &P, float v, int64_t m, int n) {
+template <typename T, typename Params>
+__device__ __forceinline__ void lin_store(const Params &P, float v, int64_t m, int n) {
     if (P.bias) v += __ldg(P.bias + n);
     if (P.z) static_cast<T *>(P.z)[m * P.ldz + n] = from_f32<T>(v);
     v = act_value(P.act, v);
@@ -97,15 +134,15 @@ __device__ __forceinline__ void lin_store(const LinParams &P, float v, int64_t m
     static_cast<T *>(P.y)[m * P.ldy + n] = from_f32<T>(v);
 }
 
-// One 128 x bn tile of D per cluster; the `splits` CTAs of the cluster share
-// its reduction (contiguous runs of 64-step blocks).  Each CTA leaves its fp32
+// One 128 x bn tile of D for each `splits` CTAs of a cluster, which share its
+// reduction (contiguous runs of 64-step blocks).  Each CTA leaves its fp32
 // partial tile in its own shared memory; after a cluster barrier CTA c reads
 // the c-th part of the tile from all of them through distributed shared
 // memory, always in rank order, and stores it.  So a product with few tiles
 // uses all SMs in one launch, without a workspace, and gives the same bits
 // each time.
 template <typename T>
-__global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_constant__ LinParams P) {
+__global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_constant__ LinGroup G) {
     extern __shared__ uint8_t lin_smem_raw[];
     __shared__ uint64_t full[kLinMaxStages], empty[kLinMaxStages], done;
     __shared__ uint32_t tmem_base;
@@ -113,7 +150,22 @@ __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_c
     uint8_t *smem = lin_smem_raw + ((1024u - (smem_u32(lin_smem_raw) & 1023u)) & 1023u);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int rank = blockIdx.x % P.splits, tile = blockIdx.x / P.splits;
+    int id = blockIdx.x / G.cluster;
+    const int place = blockIdx.x - id * G.cluster;
+    if (id >= G.tiles) {   // clusters behind the tiles': the bias gradient
+        const int c = (blockIdx.x - G.tiles * G.cluster) * kLinThreads + threadIdx.x;
+        if (c < G.bias.N) bias_grad_column(G.bias, c);
+        return;
+    }
+    const LinParams &P = G.p[id >= G.first];
+    if (id >= G.first) id -= G.first;
+    const int sub = place / P.splits, rank = place - sub * P.splits;   // which of the cluster's tiles, whose part
+    const int tile = id * (G.cluster / P.splits) + sub;
+    if (tile >= P.tiles) {   // the last cluster's empty places keep its barriers
+        cluster_sync();
+        cluster_sync();
+        return;
+    }
     const int i0 = (tile % P.tiles_i) * kLinRows, j0 = (tile / P.tiles_i) * P.bn;
     const int nkb = (P.R + kLinBK - 1) / kLinBK;
     const int kb0 = static_cast<int>(static_cast<int64_t>(nkb) * rank / P.splits);
@@ -237,7 +289,7 @@ __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_c
         tc_fence_after();
         tmem_dealloc(tmem, tmem_cols);
     }
-    if (P.splits > 1) cluster_sync();
+    if (G.cluster > 1) cluster_sync();
 
     const int outer = P.swap ? P.bn : kLinRows, inner = P.swap ? kLinRows : P.bn;
     const int m0 = P.swap ? j0 : i0, n0 = P.swap ? i0 : j0;
@@ -252,11 +304,11 @@ __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_c
             } else {
                 const uint32_t at = smem_u32(part + o * ld + n);
                 v = 0.f;
-                for (int c = 0; c < P.splits; ++c) v += ld_cluster_f32(map_to_rank(at, c));
+                for (int c = 0; c < P.splits; ++c) v += ld_cluster_f32(map_to_rank(at, sub * P.splits + c));
             }
             lin_store<T>(P, v, static_cast<int64_t>(m0) + o, n0 + n);
         }
-    if (P.splits > 1) cluster_sync();   // no CTA leaves while others read its part
+    if (G.cluster > 1) cluster_sync();   // no CTA leaves while others read its part
 }
 
 // ---------------------------------------------------------------- CTA pairs
@@ -313,8 +365,8 @@ template <typename T>
 struct PairEpilogue {
     const LinParams &P;
     uint8_t *buf;                    // two blocks
-    int lane, turn = 0;
-    __device__ PairEpilogue(const LinParams &p, uint8_t *b, int l) : P(p), buf(b), lane(l) {}
+    int lane, &turn;
+    __device__ PairEpilogue(const LinParams &p, uint8_t *b, int l, int &t) : P(p), buf(b), lane(l), turn(t) {}
 
     __device__ __forceinline__ void send(const CUtensorMap *map, const float (&v)[32], int m, int n) {
         uint8_t *dst = buf + turn * kPairBuf;
@@ -407,7 +459,7 @@ struct PairEpilogue {
 // products of the next.  All full-stage signals go to the first CTA, which
 // issues the products for both.
 template <typename T>
-__global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __grid_constant__ LinParams P) {
+__global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __grid_constant__ LinGroup G) {
     extern __shared__ uint8_t lin_smem_raw[];
     __shared__ uint64_t full[kPairMaxStages], empty[kPairMaxStages], acc_full[2], acc_empty[2];
     __shared__ uint32_t tmem_base;
@@ -416,17 +468,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t rank = cluster_ctarank();
-    const int nkb = (P.R + kLinBK - 1) / kLinBK;
     const int a_bytes = kLinRows * kLinBK * 2;
-    const int stage_bytes = a_bytes + P.b_bytes;
-    const int tiles_j = (P.J + P.bn - 1) / P.bn, tiles = P.tiles_i * tiles_j;
+    // the same for both products
+    const int bn = G.p[0].bn, b_bytes = G.p[0].b_bytes, stages = G.p[0].stages;
+    const int stage_bytes = a_bytes + b_bytes;
     const int step = gridDim.x / 2;
     volatile int *abort = &abort_flag;
 
     if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&P.amap);
-        prefetch_tensormap(&P.bmap);
-        for (int s = 0; s < P.stages; ++s) {
+        prefetch_tensormap(&G.p[0].amap);
+        prefetch_tensormap(&G.p[0].bmap);
+        for (int s = 0; s < stages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
         }
@@ -451,24 +503,29 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
 
     // tile t: bands of eight rows of tiles, column by column inside a band,
     // so that the tiles in flight share their operands in L2
-    auto place = [&](int t, int &i0, int &j0) {
+    auto place = [&](int t, int &i0, int &j0) -> const LinParams & {
+        const LinParams &P = G.p[t >= G.first];
+        if (t >= G.first) t -= G.first;
+        const int tiles_j = (P.J + bn - 1) / bn;
         const int band = t / (8 * tiles_j), in = t - band * 8 * tiles_j;
         const int rows = min(8, P.tiles_i - band * 8);
         i0 = (band * 8 + in % rows) * 2 * kLinRows;
-        j0 = (in / rows) * P.bn;
+        j0 = (in / rows) * bn;
+        return P;
     };
 
     if (warp == 0) {
         const bool issuer = elect_one();
         int s = 0, ph = 0, issued = 0;
         bool ok = true;
-        for (int t = blockIdx.x / 2; t < tiles && ok; t += step) {
+        for (int t = blockIdx.x / 2; t < G.tiles && ok; t += step) {
             int i0, j0;
-            place(t, i0, j0);
+            const LinParams &P = place(t, i0, j0);
+            const int nkb = (P.R + kLinBK - 1) / kLinBK;
             i0 += rank * kLinRows;
-            j0 += rank * (P.bn / 2);
+            j0 += rank * (bn / 2);
             for (int kb = 0; kb < nkb; ++kb) {
-                if (issued >= P.stages && !mbar_wait(&empty[s], ph ^ 1, kLinTimeoutNs, abort)) {
+                if (issued >= stages && !mbar_wait(&empty[s], ph ^ 1, kLinTimeoutNs, abort)) {
                     ok = false;
                     break;
                 }
@@ -483,7 +540,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
                         tma_load_2d_pair(a, &P.amap, bar, kb * kLinBK * 2, i0);
                     }
                     if (P.b_mn) {
-                        for (int j = 0; j < P.b_bytes / 8192; ++j)
+                        for (int j = 0; j < b_bytes / 8192; ++j)
                             tma_load_2d_pair(b + j * 8192, &P.bmap, bar, (j0 + 64 * j) * 2, kb * kLinBK);
                     } else {
                         tma_load_2d_pair(b, &P.bmap, bar, kb * kLinBK * 2, j0);
@@ -491,7 +548,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
                 }
                 __syncwarp();
                 ++issued;
-                if (++s == P.stages) {
+                if (++s == stages) {
                     s = 0;
                     ph ^= 1;
                 }
@@ -500,16 +557,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
         // the last copies land before the shared memory is given up: their
         // stages are consumed (empty) in the normal course, and given time to
         // land after a wait that ran out
-        for (int k = 0; k < min(issued, P.stages); ++k) {
+        for (int k = 0; k < min(issued, stages); ++k) {
             const int n = issued - 1 - k;
-            mbar_wait(&empty[n % P.stages], (n / P.stages) & 1, *abort ? 100000000ull : kLinTimeoutNs, nullptr);
+            mbar_wait(&empty[n % stages], (n / stages) & 1, *abort ? 100000000ull : kLinTimeoutNs, nullptr);
         }
     } else if (warp == 1 && rank == 0) {
         const bool issuer = elect_one();
-        const uint32_t a_step = P.a_mn ? 2048 : 32, b_step = P.b_mn ? 2048 : 32;
         int s = 0, ph = 0, n = 0;
         bool ok = true;
-        for (int t = blockIdx.x / 2; t < tiles && ok; t += step, ++n) {
+        for (int t = blockIdx.x / 2; t < G.tiles && ok; t += step, ++n) {
+            const LinParams &P = G.p[t >= G.first];
+            const int nkb = (P.R + kLinBK - 1) / kLinBK;
+            const uint32_t a_step = P.a_mn ? 2048 : 32, b_step = P.b_mn ? 2048 : 32;
+            const uint32_t a_lbo = P.a_mn ? 8192 : 16, b_lbo = P.b_mn ? 8192 : 16, idesc = P.idesc;
             const int b = n & 1;
             if (n >= 2 && !mbar_wait(&acc_empty[b], ((n >> 1) & 1) ^ 1, kLinTimeoutNs, abort)) break;
             tc_fence_after();
@@ -523,14 +583,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
                     const uint32_t a = smem_u32(smem + s * stage_bytes), bs = a + a_bytes;
 #pragma unroll
                     for (int k = 0; k < kLinBK / 16; ++k) {
-                        const uint64_t ad = make_smem_desc(a + k * a_step, P.a_mn ? 8192 : 16, 1024, kSwizzle128B);
-                        const uint64_t bd = make_smem_desc(bs + k * b_step, P.b_mn ? 8192 : 16, 1024, kSwizzle128B);
-                        tc_mma_f16_pair(tmem + b * P.bn, ad, bd, P.idesc, (kb > 0 || k > 0) ? 1u : 0u);
+                        const uint64_t ad = make_smem_desc(a + k * a_step, a_lbo, 1024, kSwizzle128B);
+                        const uint64_t bd = make_smem_desc(bs + k * b_step, b_lbo, 1024, kSwizzle128B);
+                        tc_mma_f16_pair(tmem + b * bn, ad, bd, idesc, (kb > 0 || k > 0) ? 1u : 0u);
                     }
                     tc_commit_pair(&empty[s]);
                 }
                 __syncwarp();
-                if (++s == P.stages) {
+                if (++s == stages) {
                     s = 0;
                     ph ^= 1;
                 }
@@ -538,27 +598,31 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
             if (issuer && ok) tc_commit_pair(&acc_full[b]);
             __syncwarp();
         }
-    } else if (warp >= 2) {
+    } else if (warp == 1) {
+        // the second CTA's: the bias gradient
+        if (G.bias.gb)
+            for (int c = blockIdx.x / 2 * 32 + lane; c < G.bias.N; c += step * 32) bias_grad_column(G.bias, c);
+    } else {
         // warps 2-9: a quadrant of the rows, half of the columns
         const int quad = warp & 3, half = (warp - 2) / 4;
-        PairEpilogue<T> out(P, smem + P.stages * stage_bytes + (warp - 2) * 2 * kPairBuf, lane);
-        int n = 0;
-        for (int t = blockIdx.x / 2; t < tiles; t += step, ++n) {
+        int n = 0, turn = 0;
+        for (int t = blockIdx.x / 2; t < G.tiles; t += step, ++n) {
             const int b = n & 1;
             int i0, j0;
-            place(t, i0, j0);
+            const LinParams &P = place(t, i0, j0);
+            PairEpilogue<T> out(P, smem + stages * stage_bytes + (warp - 2) * 2 * kPairBuf, lane, turn);
             i0 += rank * kLinRows + quad * 32;
-            j0 += half * (P.bn / 2);
+            j0 += half * (bn / 2);
             uint4 r[4];
             if (P.res && P.tma_out) out.fetch(r, i0 + lane, j0);
             if (!mbar_wait(&acc_full[b], (n >> 1) & 1, kLinTimeoutNs, abort)) break;
             tc_fence_after();
-            for (int c = 0; c < P.bn / 2; c += 32) {
+            for (int c = 0; c < bn / 2; c += 32) {
                 uint32_t acc[32];
-                tc_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * P.bn + half * (P.bn / 2) + c,
+                tc_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * bn + half * (bn / 2) + c,
                                  acc);
                 tc_wait_ld();
-                const bool last = c + 32 == P.bn / 2;
+                const bool last = c + 32 == bn / 2;
                 if (last) {   // read in full: the accumulator may be overwritten
                     tc_fence_before();
                     __syncwarp();
@@ -587,20 +651,101 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
     }
 }
 
+// ---------------------------------------------------------------- few tokens
+// One to eight tokens: the weights are read once, and that is all there is.
+// A block of eight warps computes RN features; the warps share the reduction
+// in chunks of 256 steps, a lane 8 of them from 16-byte loads (VEC), and are
+// joined in warp order.  Nothing but the loads' latency stands between the
+// launch and the last byte; the tensor-core form spends as long again on
+// filling its pipeline and joining its CTAs (14.1 us at 1 x 4096 x 4096).
+template <typename T, int MT, int RN, bool VEC>
+__global__ void __launch_bounds__(256) linear_few_kernel(const LinFew P) {
+    __shared__ float sums[8][RN * MT];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int n0 = blockIdx.x * RN;
+    const T *w = static_cast<const T *>(P.w) + static_cast<int64_t>(n0) * P.ldw, *x = static_cast<const T *>(P.x);
+    float2 acc[RN][MT];
+#pragma unroll
+    for (int r = 0; r < RN; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[r][m] = make_float2(0.f, 0.f);
+    const int chunks = (P.K + 255) / 256;
+#pragma unroll 2
+    for (int c = warp; c < chunks; c += 8) {
+        const int k = c * 256 + (VEC ? lane * 8 : lane);
+        float wv[RN][8];
+        if (VEC && k + 8 <= P.K) {
+            uint4 raw[RN];
+#pragma unroll
+            for (int r = 0; r < RN; ++r)
+                raw[r] = n0 + r < P.N ? __ldcs(reinterpret_cast<const uint4 *>(w + r * P.ldw + k)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < RN; ++r) Vec<T>::widen(raw[r], wv[r]);
+        } else {
+            const int stride = VEC ? 1 : 32;
+#pragma unroll
+            for (int r = 0; r < RN; ++r)
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    wv[r][q] = n0 + r < P.N && k + q * stride < P.K ? to_f32(w[r * P.ldw + k + q * stride]) : 0.f;
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float xv[8];
+            if (m >= P.M) continue;
+            if (VEC && k + 8 <= P.K) {
+                Vec<T>::widen(__ldg(reinterpret_cast<const uint4 *>(x + m * P.ldx + k)), xv);
+            } else {
+                const int stride = VEC ? 1 : 32;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) xv[q] = k + q * stride < P.K ? to_f32(x[m * P.ldx + k + q * stride]) : 0.f;
+            }
+#pragma unroll
+            for (int r = 0; r < RN; ++r)
+#pragma unroll
+                for (int q = 0; q < 8; q += 2)
+                    acc[r][m] = fma2(make_float2(wv[r][q], wv[r][q + 1]), make_float2(xv[q], xv[q + 1]), acc[r][m]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RN; ++r)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float s = acc[r][m].x + acc[r][m].y;
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+            if (lane == 0) sums[warp][m * RN + r] = s;
+        }
+    __syncthreads();
+    if (threadIdx.x < RN * MT) {
+        const int m = threadIdx.x / RN, n = n0 + threadIdx.x % RN;
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v += sums[k][threadIdx.x];
+        if (m < P.M && n < P.N) lin_store<T>(P, v, m, n);
+    }
+}
+
+// ---------------------------------------------------------------- passes before the products
 // Copy of a matrix whose rows are not multiples of 16 bytes into rows of
 // round_up(cols, 8) elements (the tensor maps' stride rule).
-static __global__ void linear_pack_kernel(const uint16_t *src, int64_t ld, int64_t rows, int32_t cols, uint16_t *dst,
-                                          int64_t ldd) {
-    const int64_t per = ldd / 8, n = rows * per;
-    for (int64_t e = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; e < n;
-         e += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t r = e / per;
-        const int c0 = static_cast<int>(e % per) * 8;
+struct PackJob {
+    const uint16_t *src;
+    uint16_t *dst;
+    int64_t ld, rows, ldd;
+    int32_t cols, blocks;
+};
+__device__ __forceinline__ void pack_rows(const PackJob &J, int block) {
+    const int64_t per = J.ldd / 8, n = J.rows * per;
+    for (int64_t e = block * 256ll + threadIdx.x; e < n; e += J.blocks * 256ll) {
+        const int64_t r = n <= 0x7FFFFFFF ? static_cast<uint32_t>(e) / static_cast<uint32_t>(per) : e / per;
+        const int c0 = static_cast<int>(e - r * per) * 8;
+        const uint16_t *src = J.src + r * J.ld + c0;
         uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (c0 + q < cols) w[q / 2] |= static_cast<uint32_t>(src[r * ld + c0 + q]) << (16 * (q & 1));
-        *reinterpret_cast<uint4 *>(dst + r * ldd + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (c0 + q < J.cols) w[q / 2] |= static_cast<uint32_t>(src[q]) << (16 * (q & 1));
+        *reinterpret_cast<uint4 *>(J.dst + r * J.ldd + c0) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 
@@ -608,63 +753,77 @@ static __global__ void linear_pack_kernel(const uint16_t *src, int64_t ld, int64
 // column sums of the unrounded dz over a slab of rows.  A block is 32 lanes x
 // 8 row groups; a lane owns 8 columns.  VEC: whole 16-byte loads.
 constexpr int kDzRows = 8;
+struct DzJob {
+    const void *g, *z;               // z NULL: dz = g
+    void *dz;                        // NULL: sums only
+    float *part;                     // [slabs][N], NULL: no sums
+    int64_t ldg, ldz, lddz;
+    int32_t M, N, act, slab, col_blocks, blocks;
+};
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) linear_dz_kernel(const T *g, int64_t ldg, const T *z, int64_t ldz, int32_t M,
-                                                        int32_t N, int32_t act, T *dz, int64_t lddz, float *part,
-                                                        int32_t slab) {
+__device__ __forceinline__ void dz_block(const DzJob &J, int block) {
     __shared__ float sums[kDzRows][32][9];
+    const T *g = static_cast<const T *>(J.g), *z = static_cast<const T *>(J.z);
+    T *dz = static_cast<T *>(J.dz);
+    const int by = block / J.col_blocks, bx = block - by * J.col_blocks;
     const int lane = threadIdx.x % 32, ty = threadIdx.x / 32;
-    const int c0 = (blockIdx.x * 32 + lane) * 8;
-    const int r1 = static_cast<int>(min(static_cast<int64_t>(M), (blockIdx.y + static_cast<int64_t>(1)) * slab));
+    const int c0 = (bx * 32 + lane) * 8;
+    const int r1 = static_cast<int>(min(static_cast<int64_t>(J.M), (by + static_cast<int64_t>(1)) * J.slab));
     float acc[8] = {};
-    if (c0 < N) {
-        for (int64_t r = static_cast<int64_t>(blockIdx.y) * slab + ty; r < r1; r += kDzRows) {
+    if (c0 < J.N) {
+#pragma unroll 2
+        for (int64_t r = static_cast<int64_t>(by) * J.slab + ty; r < r1; r += kDzRows) {
             float v[8], zv[8] = {};
-            if (VEC && c0 + 8 <= N) {
-                Vec<T>::widen(*reinterpret_cast<const uint4 *>(g + r * ldg + c0), v);
-                if (z) Vec<T>::widen(*reinterpret_cast<const uint4 *>(z + r * ldz + c0), zv);
+            if (VEC && c0 + 8 <= J.N) {
+                Vec<T>::widen(*reinterpret_cast<const uint4 *>(g + r * J.ldg + c0), v);
+                if (z) Vec<T>::widen(*reinterpret_cast<const uint4 *>(z + r * J.ldz + c0), zv);
             } else {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    v[q] = c0 + q < N ? to_f32(g[r * ldg + c0 + q]) : 0.f;
-                    if (z && c0 + q < N) zv[q] = to_f32(z[r * ldz + c0 + q]);
+                    v[q] = c0 + q < J.N ? to_f32(g[r * J.ldg + c0 + q]) : 0.f;
+                    if (z && c0 + q < J.N) zv[q] = to_f32(z[r * J.ldz + c0 + q]);
                 }
             }
             if (z) {
                 float s[8];
-                act_slopes(act, zv, s);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) v[q] *= s[q];
+                act_slopes(J.act, zv, s);
+                mul_to(v, s);
             }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) acc[q] += v[q];
-            if (dz) *reinterpret_cast<uint4 *>(dz + r * lddz + c0) = Vec<T>::narrow(v);   // lddz = round_up(N, 8)
+            add_to(acc, v);
+            if (dz) *reinterpret_cast<uint4 *>(dz + r * J.lddz + c0) = Vec<T>::narrow(v);   // lddz = round_up(N, 8)
         }
     }
-    if (part == nullptr) return;
+    if (J.part == nullptr) return;
 #pragma unroll
     for (int q = 0; q < 8; ++q) sums[ty][lane][q] = acc[q];
     __syncthreads();
     // 256 columns of the block, one per thread
-    const int l = threadIdx.x / 8, q = threadIdx.x % 8, c = (blockIdx.x * 32 + l) * 8 + q;
-    if (c < N) {
+    const int l = threadIdx.x / 8, q = threadIdx.x % 8, c = (bx * 32 + l) * 8 + q;
+    if (c < J.N) {
         float s = 0.f;
         for (int k = 0; k < kDzRows; ++k) s += sums[k][l][q];
-        part[static_cast<int64_t>(blockIdx.y) * N + c] = s;
+        J.part[static_cast<int64_t>(by) * J.N + c] = s;
     }
 }
 
-// gb[n] = sum of the slabs' partial sums, in slab order.
-static __global__ void linear_bias_grad_kernel(const float *part, int32_t slabs, int32_t N, float *gb) {
+// All that has to be done before a layer's products, in one launch: the dz
+// blocks, then those of up to two copies.
+struct LinPrep {
+    DzJob dz;
+    PackJob pack[2];
+};
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) linear_prep_kernel(const __grid_constant__ LinPrep P) {
+    int b = blockIdx.x;
+    if (b < P.dz.blocks) return dz_block<T, VEC>(P.dz, b);
+    b -= P.dz.blocks;
+    const int which = b >= P.pack[0].blocks;
+    pack_rows(P.pack[which], which ? b - P.pack[0].blocks : b);
+}
+
+static __global__ void linear_bias_grad_kernel(const BiasGrad b) {
     const int c = blockIdx.x * blockDim.x + threadIdx.x;
-    if (c >= N) return;
-    float s[4] = {};
-    int k = 0;
-    for (; k + 4 <= slabs; k += 4)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) s[q] += part[static_cast<int64_t>(k + q) * N + c];
-    for (; k < slabs; ++k) s[0] += part[static_cast<int64_t>(k) * N + c];
-    gb[c] = (s[0] + s[1]) + (s[2] + s[3]);
+    if (c < b.N) bias_grad_column(b, c);
 }
 
 }  // namespace mqc

@@ -100,10 +100,12 @@ def test_linear_refusals(mqc):
         assert fwd(lin(), **{k: ODD}) == -5, k
     assert fwd(lin(ldx=15)) == -1 and fwd(lin(ldw=8)) == -1 and fwd(lin(ldy=7)) == -1
     assert fwd(lin(ldr=7), r=P16) == -1 and fwd(lin(ldz=0), z=P16) == -1
-    assert fwd(lin(ldx=17)) == -6                   # rows of 34 bytes: a padded copy is needed
-    assert mqc.mqc_linear_fwd_workspace_bytes(lin()) == 0
-    assert mqc.mqc_linear_fwd_workspace_bytes(lin(ldx=17)) == 256
-    assert fwd(lin(ldx=17), ws=ODD, n=256) == -5
+    many = dict(M=16, ldx=17)                       # rows of 34 bytes: a padded copy is needed
+    assert fwd(lin(**many)) == -6
+    assert mqc.mqc_linear_fwd_workspace_bytes(lin(M=16)) == 0
+    assert mqc.mqc_linear_fwd_workspace_bytes(lin(**many)) == 512
+    assert mqc.mqc_linear_fwd_workspace_bytes(lin(ldx=17)) == 0     # few tokens are read as they are
+    assert fwd(lin(**many), ws=ODD, n=512) == -5
     bwd = lambda l, g=P16, z=P16, x=P16, w=P16, gx=P16, gw=P16, gb=P16, ws=None, n=0: mqc.mqc_linear_bwd(  # noqa: E731
         l, g, z, x, w, gx, gw, gb, ws, n, None)
     assert bwd(lin()) == -6 and bwd(lin(act=2)) == -6
