@@ -56,7 +56,14 @@ struct Product {
     int64_t kblocks() const { return ceil_div(red, kLinBK); }
 };
 
-// What both kernels need besides the tiling; `a_rows`, `b_rows`: box rows.
+// Whether the rows of the outputs and the residual are whole 16-byte vectors
+// (a TMA store clips its rows at whole 16 bytes only).
+bool vector_rows(const Product &p) {
+    const Epilogue &E = p.E;
+    return p.features % 8 == 0 && E.ldy % 8 == 0 && (!E.z || E.ldz % 8 == 0) && (!E.res || E.ldr % 8 == 0);
+}
+
+// What both kernels need besides the tiling.
 mqc_status fill_params(LinParams &P, const Product &p, bool bf16, int rows, bool pair) {
     const Operand &A = P.swap ? p.W : p.X, &B = P.swap ? p.X : p.W;
     const Epilogue &E = p.E;
@@ -64,7 +71,7 @@ mqc_status fill_params(LinParams &P, const Product &p, bool bf16, int rows, bool
     P.a_mn = A.mn;
     P.b_mn = B.mn;
     P.idesc = make_idesc_f16(bf16, A.mn, B.mn, rows, P.bn);
-    P.tma_out = pair && E.ldy % 8 == 0 && (!E.z || E.ldz % 8 == 0) && (!E.res || E.ldr % 8 == 0);
+    P.vec_out = vector_rows(p);
     P.act = E.act;
     P.bias = E.bias;
     P.res = E.res;
@@ -78,8 +85,8 @@ mqc_status fill_params(LinParams &P, const Product &p, bool bf16, int rows, bool
     if (st != MQC_OK) return st;
     st = B.mn ? encode_matrix_map(&P.bmap, B.p, p.red, P.J, B.ld, kLinBK)
               : encode_matrix_map(&P.bmap, B.p, P.J, p.red, B.ld, pair ? P.bn / 2 : P.bn);
-    if (st == MQC_OK && P.tma_out) st = encode_matrix_map(&P.ymap, E.y, P.I, P.J, E.ldy, 32, 64);
-    if (st == MQC_OK && P.tma_out && E.z) st = encode_matrix_map(&P.zmap, E.z, P.I, P.J, E.ldz, 32, 64);
+    if (st == MQC_OK && pair && P.vec_out) st = encode_matrix_map(&P.ymap, E.y, P.I, P.J, E.ldy, 32, 64);
+    if (st == MQC_OK && pair && P.vec_out && E.z) st = encode_matrix_map(&P.zmap, E.z, P.I, P.J, E.ldz, 32, 64);
     return st;
 }
 
@@ -106,6 +113,66 @@ mqc_status launch_group(const LinGroup &G, bool pair, bool bf16, int64_t grid, i
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear kernel launch");
 }
 
+// The tiling of a product on single tiles, and its estimated time in us, from
+// a fit to some 300 measured combinations on a B200 (within 20%): 4.4 for a
+// launch, 2.7 for a joined reduction, 3.8 for each further round of resident
+// CTAs, and for each CTA of the busiest SM 0.16 a stage of 64 steps plus 0.27
+// by its columns (of 256), and 6.3 by its columns to finish them.  Clusters of
+// four and eight CTAs, an SM each, find room for fewer (in whole groups of
+// SMs).
+struct TilePlan {
+    int32_t bn, splits;
+    int64_t tiles;
+    double us;
+};
+TilePlan plan_tiles(const Product &p, int sms) {
+    const bool swap = p.swap();
+    const int64_t rows = ceil_div(swap ? p.features : p.tokens, kLinRows), cols = swap ? p.tokens : p.features;
+    TilePlan best{0, 0, 0, 1e300};
+    for (int bn = 256; bn >= 32; bn /= 2) {
+        TilePlan t{bn, 1, 0, 0.0};
+        if (swap) {   // all the tokens in one tile, so that the weights are read once
+            t.bn = static_cast<int32_t>(round_up(cols, 16));
+            bn = 32;
+        } else if (bn > 32 && bn / 2 >= cols) {
+            continue;
+        }
+        t.tiles = rows * ceil_div(cols, t.bn);
+        for (t.splits = 1; t.splits <= 8 && t.splits <= p.kblocks(); t.splits *= 2) {
+            const int64_t room = t.splits == 8 ? sms * 13 / 16 : (t.splits == 4 ? sms * 9 / 10 : sms);
+            const int64_t on_sm = ceil_div(t.tiles * t.splits, room), kb = ceil_div(p.kblocks(), t.splits);
+            const int64_t rounds = t.bn <= 64 ? ceil_div(on_sm, 2) : on_sm;   // two narrow tiles share an SM
+            const double wide = t.bn / 256.0;
+            t.us = 4.4 + (t.splits > 1 ? 2.7 : 0.0) + (rounds - 1) * 3.8 +
+                   on_sm * (kb * (0.16 + 0.27 * wide) + 6.3 * wide / t.splits);
+            if (t.us < best.us) best = t;
+        }
+    }
+    return best;
+}
+
+// On CTA pairs: the busiest pair's 64-step blocks at 0.40 (256 columns) or 0.32,
+// the launch and the last tile's output.
+struct PairPlan {
+    int32_t bn;
+    double us;
+};
+int64_t pair_tiles(const Product &p, int bn) { return ceil_div(p.tokens, 2 * kLinRows) * ceil_div(p.features, bn); }
+PairPlan plan_pairs(const Product *const *p, int count, int pairs) {
+    PairPlan best{0, 1e300};
+    for (int bn = 256; bn >= 128; bn /= 2) {
+        const int64_t t0 = pair_tiles(*p[0], bn), t1 = count > 1 ? pair_tiles(*p[1], bn) : 0;
+        int64_t most = 0;   // tiles are dealt out in turn
+        for (int c = 0; c < pairs; ++c) {
+            const int64_t n0 = (t0 - c + pairs - 1) / pairs, n = (t0 + t1 - c + pairs - 1) / pairs;
+            most = std::max(most, n0 * p[0]->kblocks() + (count > 1 ? (n - n0) * p[1]->kblocks() : 0));
+        }
+        const double us = 4.5 + most * (bn == 256 ? 0.40 : 0.32) + bn / 85.0;
+        if (us < best.us) best = PairPlan{bn, us};
+    }
+    return best;
+}
+
 // One or two products on CTA pairs, the longer reduction's tiles first (they
 // are dealt out in turn, so the shorter ones even out the end).
 mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool bf16, const DeviceLimits &d,
@@ -113,22 +180,10 @@ mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool 
     const int pairs = d.sms / 2;
     const Product *order[2] = {&p[0], count > 1 ? &p[1] : nullptr};
     if (count > 1 && p[1].kblocks() > p[0].kblocks()) std::swap(order[0], order[1]);
-    // 256 or 128 columns: the shorter way for the busiest pair, a narrow tile
-    // counted as 0.6 of a wide one
-    auto tiles_of = [](const Product &q, int bn) { return ceil_div(q.tokens, 2 * kLinRows) * ceil_div(q.features, bn); };
-    auto busiest = [&](int bn) {
-        const int64_t t0 = tiles_of(*order[0], bn), t1 = count > 1 ? tiles_of(*order[1], bn) : 0;
-        int64_t most = 0;
-        for (int c = 0; c < pairs; ++c) {
-            const int64_t n0 = (t0 - c + pairs - 1) / pairs, n = (t0 + t1 - c + pairs - 1) / pairs;
-            most = std::max(most, n0 * order[0]->kblocks() + (count > 1 ? (n - n0) * order[1]->kblocks() : 0));
-        }
-        return most;
-    };
-    const int bn = busiest(128) * 6 < busiest(256) * 10 ? 128 : 256;
+    const int bn = plan_pairs(order, count, pairs).bn;
     const int b_bytes = bn / 2 * kLinBK * 2, stage = kLinRows * kLinBK * 2 + b_bytes;
-    const int stages = std::min(kPairMaxStages, (d.max_smem - 2048 - 1024 - kPairStaging) / stage);
     LinGroup G{};
+    const int stages = std::min(kPairMaxStages, (d.max_smem - 2048 - 1024 - kPairStaging) / stage);
     G.bias = bias;
     int64_t tiles = 0;
     for (int i = 0; i < count; ++i) {
@@ -140,7 +195,7 @@ mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool 
         P.stages = stages;
         P.splits = 1;
         P.tiles_i = static_cast<int32_t>(ceil_div(P.I, 2 * kLinRows));
-        tiles += tiles_of(*order[i], bn);
+        tiles += pair_tiles(*order[i], bn);
         if (tiles > (int64_t(1) << 30)) return fail(MQC_ERR_INVALID, "linear: too many tiles");
         if (i == 0) G.first = static_cast<int32_t>(tiles);
         mqc_status st = fill_params(P, *order[i], bf16, 2 * kLinRows, true);
@@ -165,21 +220,13 @@ mqc_status launch_tiles(const Product *p, int count, const BiasGrad &bias, bool 
         P.I = P.swap ? p[i].features : p[i].tokens;
         P.J = P.swap ? p[i].tokens : p[i].features;
         P.tiles_i = static_cast<int32_t>(ceil_div(P.I, kLinRows));
-        // the widest column tile that still gives every SM one; all the tokens
-        // of the swapped form in one tile, so that the weights are read once
-        if (P.swap) {
-            P.bn = static_cast<int32_t>(round_up(P.J, 16));
-        } else {
-            P.bn = 256;
-            while (P.bn > 32 && (P.bn / 2 >= P.J || P.tiles_i * ceil_div(P.J, P.bn) < d.sms)) P.bn /= 2;
-        }
-        const int64_t tiles = P.tiles_i * ceil_div(P.J, P.bn);
-        if (tiles > (int64_t(1) << 30) / 16) return fail(MQC_ERR_INVALID, "linear: too many tiles");
-        P.tiles = static_cast<int32_t>(tiles);
-        P.splits = 1;
-        while (P.splits < 8 && tiles * P.splits < d.sms && p[i].kblocks() / (2 * P.splits) >= 2) P.splits *= 2;
+        const TilePlan t = plan_tiles(p[i], d.sms);
+        if (t.tiles > (int64_t(1) << 30) / 16) return fail(MQC_ERR_INVALID, "linear: too many tiles");
+        P.bn = t.bn;
+        P.tiles = static_cast<int32_t>(t.tiles);
+        P.splits = t.splits;
         G.cluster = std::max(G.cluster, P.splits);
-        ctas += tiles * P.splits;
+        ctas += t.tiles * P.splits;
     }
     int smem = 0;
     for (int i = 0; i < count; ++i) {
@@ -187,7 +234,7 @@ mqc_status launch_tiles(const Product *p, int count, const BiasGrad &bias, bool 
         const bool b_mn = P.swap ? p[i].X.mn : p[i].W.mn;
         P.b_bytes = (b_mn ? static_cast<int>(round_up(P.bn, 64)) : P.bn) * kLinBK * 2;
         const int stage = kLinRows * kLinBK * 2 + P.b_bytes;
-        const int part = P.swap ? P.bn * kLinRows * 4 : kLinRows * (P.bn + 1) * 4;
+        const int part = P.swap ? P.bn * kLinRows * 4 : kLinRows * (P.bn + 4) * 4;
         const int room = d.max_smem - 2048 - 1024;
         const int share = ctas > d.sms && P.bn <= 64 ? room / 2 - 512 : room;
         P.stages = std::max(1, std::min({kLinMaxStages, share / stage,
@@ -203,20 +250,20 @@ mqc_status launch_tiles(const Product *p, int count, const BiasGrad &bias, bool 
 }
 
 // The products of a call, and its bias gradient's last sums beside them: in
-// one launch when the same kernel suits them.  CTA pairs once their 256-row
-// tiles fill most of the SM pairs.
+// one launch when the same kernel suits them.
 mqc_status launch_products(const Product *p, int count, const BiasGrad &bias, int32_t dtype, const DeviceLimits &d,
                            cudaStream_t stream) {
     const bool bf16 = dtype == MQC_BF16;
-    int64_t narrow = 0;
-    for (int i = 0; i < count; ++i)
-        narrow += p[i].swap() ? 0 : ceil_div(p[i].tokens, 2 * kLinRows) * ceil_div(p[i].features, 128);
-    const bool enough = narrow >= d.sms / 2 * 3 / 4;
-    if (count > 1 && p[0].swap() != p[1].swap()) {
+    bool pairs[2] = {};
+    for (int i = 0; i < count; ++i) {
+        const Product *one = &p[i];
+        pairs[i] = !one->swap() && plan_pairs(&one, 1, d.sms / 2).us < plan_tiles(*one, d.sms).us;
+    }
+    if (count > 1 && pairs[0] != pairs[1]) {
         mqc_status st = launch_products(p, 1, bias, dtype, d, stream);
         return st != MQC_OK ? st : launch_products(p + 1, 1, BiasGrad{}, dtype, d, stream);
     }
-    return enough ? launch_pairs(p, count, bias, bf16, d, stream) : launch_tiles(p, count, bias, bf16, d, stream);
+    return pairs[0] ? launch_pairs(p, count, bias, bf16, d, stream) : launch_tiles(p, count, bias, bf16, d, stream);
 }
 
 // Bytes of a padded copy of a rows x cols matrix, and whether one is needed.
@@ -257,10 +304,17 @@ mqc_status launch_prep(const LinPrep &prep, int32_t dtype, cudaStream_t stream) 
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear_prep_kernel launch");
 }
 
-// One to eight tokens (linear_few_kernel).  Four features a block (two beyond
-// two tokens, for the registers) where that still leaves a block or more an
-// SM several times over, else one.
-constexpr int kFewTokens = 8;
+// One to eight tokens (linear_few_kernel).  Four features a block where that
+// still leaves several blocks an SM, else one.
+// One or two tokens always; up to four (eight, if the tensor-core form would
+// have to copy operands first) where the weights are few: at 4096 x 4096 it
+// takes 8.4 us with one token, 11.0 with two and 14.6 with three, the tensor
+// cores 11.4 with any up to 16; at 1024 x 1024 2.7, 3.0 and 4.5 against 6.1.
+bool few_tokens(const mqc_linear *l) {
+    if (l->M <= 2) return true;
+    if (int64_t(l->N) * l->K > int64_t(1) << 22) return false;
+    return l->M <= 4 || (l->M <= 8 && (needs_pack(l->ldx) || needs_pack(l->ldw)));
+}
 template <typename T, int MT, int RN>
 void launch_few_as(const LinFew &P, bool vec, cudaStream_t s) {
     const unsigned grid = static_cast<unsigned>(ceil_div(P.N, RN));
@@ -272,8 +326,8 @@ void launch_few(const LinFew &P, cudaStream_t s) {
     const bool vec = P.ldw % 8 == 0 && (P.M == 1 || P.ldx % 8 == 0), wide = P.N >= 2048;
     if (P.M == 1) wide ? launch_few_as<T, 1, 4>(P, vec, s) : launch_few_as<T, 1, 1>(P, vec, s);
     else if (P.M == 2) wide ? launch_few_as<T, 2, 4>(P, vec, s) : launch_few_as<T, 2, 1>(P, vec, s);
-    else if (P.M <= 4) wide ? launch_few_as<T, 4, 2>(P, vec, s) : launch_few_as<T, 4, 1>(P, vec, s);
-    else wide ? launch_few_as<T, 8, 2>(P, vec, s) : launch_few_as<T, 8, 1>(P, vec, s);
+    else if (P.M <= 4) wide ? launch_few_as<T, 4, 4>(P, vec, s) : launch_few_as<T, 4, 1>(P, vec, s);
+    else wide ? launch_few_as<T, 8, 4>(P, vec, s) : launch_few_as<T, 8, 1>(P, vec, s);
 }
 
 mqc_status check_linear(const mqc_linear *l, const char *name) {
@@ -303,12 +357,12 @@ mqc_status check_workspace(const char *name, const void *ws, size_t bytes, size_
     return MQC_OK;
 }
 
-// Row slabs of the dz pass: enough blocks for two waves of 8 blocks an SM, at
+// Row slabs of the dz pass: all blocks (three on each of 148 SMs) at once, at
 // least 32 rows each.  A function of the sizes alone, so that the workspace
 // query needs no device.
 void dz_slabs(int64_t M, int64_t N, int32_t &slab, int32_t &slabs) {
     const int64_t col_blocks = ceil_div(N, 256);
-    const int64_t want = std::max<int64_t>(1, 1184 / col_blocks);
+    const int64_t want = std::max<int64_t>(1, 148 * 3 / col_blocks);
     slab = static_cast<int32_t>(std::max<int64_t>(32, ceil_div(M, want)));
     slabs = static_cast<int32_t>(ceil_div(M, slab));
 }
@@ -321,7 +375,7 @@ using namespace mqc;
 extern "C" {
 
 size_t mqc_linear_fwd_workspace_bytes(const mqc_linear *l) {
-    if (check_linear(l, "linear_fwd") != MQC_OK || l->M <= kFewTokens) return 0;
+    if (check_linear(l, "linear_fwd") != MQC_OK || few_tokens(l)) return 0;
     return (needs_pack(l->ldx) ? packed_bytes(l->M, l->K) : 0) + (needs_pack(l->ldw) ? packed_bytes(l->N, l->K) : 0);
 }
 
@@ -342,7 +396,7 @@ mqc_status mqc_linear_fwd(const mqc_linear *l, const void *x, const void *w, con
     DeviceLimits d;
     if ((st = device_limits(&d)) != MQC_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (l->M <= kFewTokens) {
+    if (few_tokens(l)) {
         LinFew P{x, w, bias, residual, y, z, l->ldx, l->ldw, l->ldr, l->ldy, l->ldz, l->M, l->N, l->K, l->act};
         if (l->dtype == MQC_BF16) launch_few<__nv_bfloat16>(P, s);
         else launch_few<__half>(P, s);

@@ -35,7 +35,7 @@ struct LinParams {
     int32_t b_bytes;                 // bytes of B per stage
     uint32_t idesc;
     int32_t act;
-    int32_t tma_out;                 // y (and z) leave through their maps
+    int32_t vec_out;                 // output (and residual) rows are whole 16-byte vectors
     const float *bias;               // per feature
     const void *res;
     void *y, *z;
@@ -109,12 +109,6 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(saddr), "r"(rank));
     return a;
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 struct LinFew {
     const void *x, *w;
     const float *bias;
@@ -134,13 +128,93 @@ __device__ __forceinline__ void lin_store(const Params &P, float v, int64_t m, i
     static_cast<T *>(P.y)[m * P.ldy + n] = from_f32<T>(v);
 }
 
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+                 : "memory");
+}
+
+// A CTA's share of a tile: `rows` tokens from m0 on, `width` features from n0
+// on, summed from the SPLITS partial copies [rows_all][ld] in its shared memory
+// in order, finished and stored.  VEC: eight features a thread, 16-byte stores
+// (a warp's store of 32 single elements takes the load-store unit as long as
+// one of 32 vectors); else one feature a lane, four tokens at a time.
+template <typename T, int SPLITS, bool VEC>
+__device__ __forceinline__ void tile_epilogue(const LinParams &P, const float *part, int ld, int rows_all, int rows,
+                                              int width, int64_t m0, int n0) {
+    const T *res = static_cast<const T *>(P.res);
+    T *y = static_cast<T *>(P.y), *z = static_cast<T *>(P.z);
+    if (VEC) {
+        const int groups = width / 8;
+        for (int e = threadIdx.x; e < rows * groups; e += kLinThreads) {
+            const int o = e / groups, n = (e - o * groups) * 8;
+            const int64_t m = m0 + o;
+            uint4 r = make_uint4(0, 0, 0, 0);
+            if (res) r = *reinterpret_cast<const uint4 *>(res + m * P.ldr + n0 + n);
+            float v[8];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 s = *reinterpret_cast<const float4 *>(part + o * ld + n + 4 * h);
+#pragma unroll
+                for (int c = 1; c < SPLITS; ++c) {
+                    const float4 t = *reinterpret_cast<const float4 *>(part + (c * rows_all + o) * ld + n + 4 * h);
+                    s.x += t.x, s.y += t.y, s.z += t.z, s.w += t.w;
+                }
+                if (P.bias) {
+                    const float4 b = __ldg(reinterpret_cast<const float4 *>(P.bias + n0 + n) + h);
+                    s.x += b.x, s.y += b.y, s.z += b.z, s.w += b.w;
+                }
+                v[4 * h] = s.x, v[4 * h + 1] = s.y, v[4 * h + 2] = s.z, v[4 * h + 3] = s.w;
+            }
+            if (z) *reinterpret_cast<uint4 *>(z + m * P.ldz + n0 + n) = Vec<T>::narrow(v);
+            act_values(P.act, v);
+            if (res) {
+                float f[8];
+                Vec<T>::widen(r, f);
+                add_to(v, f);
+            }
+            *reinterpret_cast<uint4 *>(y + m * P.ldy + n0 + n) = Vec<T>::narrow(v);
+        }
+        return;
+    }
+    constexpr int U = 4;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    for (int n = lane; n < width; n += 32) {
+        const float bias = P.bias ? __ldg(P.bias + n0 + n) : 0.f;
+        for (int o = warp * U; o < rows; o += kLinThreads / 32 * U) {
+            float r[U], s[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                r[u] = res && o + u < rows ? to_f32(res[(m0 + o + u) * P.ldr + n0 + n]) : 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                s[u] = 0.f;
+                if (o + u < rows) {
+                    s[u] = part[(o + u) * ld + n];
+#pragma unroll
+                    for (int c = 1; c < SPLITS; ++c) s[u] += part[(c * rows_all + o + u) * ld + n];
+                    s[u] += bias;
+                    if (z) z[(m0 + o + u) * P.ldz + n0 + n] = from_f32<T>(s[u]);
+                }
+            }
+            act_values(P.act, s);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (o + u < rows) y[(m0 + o + u) * P.ldy + n0 + n] = from_f32<T>(res ? s[u] + r[u] : s[u]);
+        }
+    }
+}
+
 // One 128 x bn tile of D for each `splits` CTAs of a cluster, which share its
-// reduction (contiguous runs of 64-step blocks).  Each CTA leaves its fp32
-// partial tile in its own shared memory; after a cluster barrier CTA c reads
-// the c-th part of the tile from all of them through distributed shared
-// memory, always in rank order, and stores it.  So a product with few tiles
-// uses all SMs in one launch, without a workspace, and gives the same bits
-// each time.
+// reduction (contiguous runs of 64-step blocks).  Once all of them are through
+// with their stages, each sends the c-th part of its fp32 partial tile to the
+// shared memory of the c-th (writes, which nobody waits for; reading the parts
+// back from their owners spent most of a small product's time on the latency
+// of distributed shared memory), and after another barrier every CTA sums what
+// it got in rank order and stores it.  So a product with few tiles uses all
+// SMs in one launch, without a workspace, and gives the same bits each time.
 template <typename T>
 __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_constant__ LinGroup G) {
     extern __shared__ uint8_t lin_smem_raw[];
@@ -262,53 +336,68 @@ __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_c
         __syncwarp();
     }
 
-    // partial tile -> shared memory as [outer][inner], the output's row index
-    // (token) outer: i outer in the plain form, j outer in the swapped one
+    // partial tile -> [outer][inner], the output's row index (token) outer: i
+    // outer in the plain form, j outer in the swapped one; the CTA of rank c
+    // gets rows [c, c + 1) * share of all partial tiles, [rank][share][ld]
     float *part = reinterpret_cast<float *>(smem);
-    const int ld = P.swap ? kLinRows : P.bn + 1;   // odd stride: lanes write distinct banks
+    const int outer = P.swap ? P.bn : kLinRows, share = outer / P.splits;
+    const int ld = P.swap ? kLinRows : P.bn + 4;   // 16-byte rows, and lanes' vectors in distinct banks
     if (warp >= 2) {
         mbar_wait(&done, 0, kLinTimeoutNs, abort);
         tc_fence_after();
+    }
+    __syncthreads();
+    if (G.cluster > 1) cluster_sync();   // nobody's stages are in use any more
+    if (warp >= 2) {
         const int quad = warp & 3, i = quad * 32 + lane;
+        const uint32_t base = smem_u32(part);
+        const int mine = i / share;      // plain form: the CTA that gets row i
+        const uint32_t row = P.swap ? 0 : map_to_rank(base, sub * P.splits + mine) +
+                                              4 * ((rank * share + i - mine * share) * ld);
         for (int c = 0; c < P.bn; c += 16) {
             uint32_t r[16];
             tc_ld_32x32b_x16(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, r);
             tc_wait_ld();
             if (P.swap) {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) part[(c + q) * ld + i] = __uint_as_float(r[q]);
+                for (int q = 0; q < 16; ++q) {
+                    const int o = c + q, owner = o / share;
+                    st_cluster_f32(map_to_rank(base, sub * P.splits + owner) +
+                                       4 * ((rank * share + o - owner * share) * ld + i),
+                                   __uint_as_float(r[q]));
+                }
             } else {
 #pragma unroll
-                for (int q = 0; q < 16; ++q) part[i * ld + c + q] = __uint_as_float(r[q]);
+                for (int q = 0; q < 16; q += 4)
+                    st_cluster_v4(row + 4 * (c + q), __uint_as_float(r[q]), __uint_as_float(r[q + 1]),
+                                  __uint_as_float(r[q + 2]), __uint_as_float(r[q + 3]));
             }
         }
         tc_fence_before();
     }
     __syncthreads();
+    if (G.cluster > 1) cluster_sync();   // all parts have arrived
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, tmem_cols);
     }
-    if (G.cluster > 1) cluster_sync();
 
-    const int outer = P.swap ? P.bn : kLinRows, inner = P.swap ? kLinRows : P.bn;
-    const int m0 = P.swap ? j0 : i0, n0 = P.swap ? i0 : j0;
+    const int inner = P.swap ? kLinRows : P.bn;
+    const int64_t m0 = (P.swap ? j0 : i0) + rank * share;
+    const int n0 = P.swap ? i0 : j0;
     const int M = P.swap ? P.J : P.I, N = P.swap ? P.I : P.J;
-    const int o0 = outer * rank / P.splits, o1 = min(outer * (rank + 1) / P.splits, M - m0);
-    const int width = min(inner, N - n0);
-    for (int o = o0 + warp; o < o1; o += kLinThreads / 32)
-        for (int n = lane; n < width; n += 32) {
-            float v;
-            if (P.splits == 1) {
-                v = part[o * ld + n];
-            } else {
-                const uint32_t at = smem_u32(part + o * ld + n);
-                v = 0.f;
-                for (int c = 0; c < P.splits; ++c) v += ld_cluster_f32(map_to_rank(at, sub * P.splits + c));
-            }
-            lin_store<T>(P, v, static_cast<int64_t>(m0) + o, n0 + n);
-        }
-    if (G.cluster > 1) cluster_sync();   // no CTA leaves while others read its part
+    const int rows = static_cast<int>(min(static_cast<int64_t>(share), M - m0)), width = min(inner, N - n0);
+    if (P.vec_out) {
+        if (P.splits == 1) tile_epilogue<T, 1, true>(P, part, ld, share, rows, width, m0, n0);
+        else if (P.splits == 2) tile_epilogue<T, 2, true>(P, part, ld, share, rows, width, m0, n0);
+        else if (P.splits == 4) tile_epilogue<T, 4, true>(P, part, ld, share, rows, width, m0, n0);
+        else tile_epilogue<T, 8, true>(P, part, ld, share, rows, width, m0, n0);
+    } else {
+        if (P.splits == 1) tile_epilogue<T, 1, false>(P, part, ld, share, rows, width, m0, n0);
+        else if (P.splits == 2) tile_epilogue<T, 2, false>(P, part, ld, share, rows, width, m0, n0);
+        else if (P.splits == 4) tile_epilogue<T, 4, false>(P, part, ld, share, rows, width, m0, n0);
+        else tile_epilogue<T, 8, false>(P, part, ld, share, rows, width, m0, n0);
+    }
 }
 
 // ---------------------------------------------------------------- CTA pairs
@@ -358,7 +447,8 @@ constexpr int kPairStaging = 8 * 2 * kPairBuf;
 // The epilogue of one warp: 32 tokens (one a lane) x 32 features.  A lane
 // stores its 64 bytes of y (and z) to a shared-memory block in the 64-byte
 // swizzle of the output's tensor map, which the TMA writes out as whole
-// sectors, clipped at the matrix's last row and (to 16 bytes) its last column.  (Stores of 16 bytes a lane straight
+// sectors, clipped at the matrix's ends (whole 16 bytes of a row only, which
+// is why matrices of other widths take the other form).  (Stores of 16 bytes a lane straight
 // to global memory, rows apart, were half sectors: with z they cost 40 us of
 // 221 at 8192 x 4096 x 4096.)
 template <typename T>
@@ -386,22 +476,12 @@ struct PairEpilogue {
         __syncwarp();
     }
 
-    // The lane's 64 bytes of the residual; elements past the row's end are
-    // not read.
+    // The lane's 64 bytes of the residual (its rows are whole 16-byte vectors).
     __device__ __forceinline__ void fetch(uint4 (&r)[4], int64_t m, int n) const {
         const T *res = static_cast<const T *>(P.res) + m * P.ldr + n;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            r[q] = make_uint4(0, 0, 0, 0);
-            if (m < P.I && n + 8 * q + 8 <= P.J) {
-                r[q] = reinterpret_cast<const uint4 *>(res)[q];
-            } else if (m < P.I) {
-                float e[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) e[k] = n + 8 * q + k < P.J ? to_f32(res[8 * q + k]) : 0.f;
-                r[q] = Vec<T>::narrow(e);
-            }
-        }
+        for (int q = 0; q < 4; ++q)
+            r[q] = m < P.I && n + 8 * q < P.J ? reinterpret_cast<const uint4 *>(res)[q] : make_uint4(0, 0, 0, 0);
     }
 
     __device__ __forceinline__ void block(const uint32_t (&acc)[32], const uint4 (&r)[4], int m0, int n) {
@@ -436,9 +516,10 @@ struct PairEpilogue {
     }
 
     // Output rows of other strides: the accumulators change lanes through
-    // shared memory (fp32, a row's elements rotated by its number, so that
-    // neither side meets bank conflicts) and a warp writes 32 features of one
-    // token at a time.
+    // shared memory (fp32; a row's elements in an order exclusive-ored with its
+    // number, so that neither side meets bank conflicts), and a warp writes 32
+    // features of one token at a time.  (64 features in 4-byte words took
+    // longer: the odd rows' ends need stores of their own.)
     __device__ __forceinline__ void block_any(const uint32_t (&acc)[32], int64_t m0, int n) {
         float *f = reinterpret_cast<float *>(buf);
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -446,8 +527,35 @@ struct PairEpilogue {
 #pragma unroll
         for (int e = 0; e < 32; ++e) f[lane * 32 + (e ^ lane)] = __uint_as_float(acc[e]);
         __syncwarp();
-        if (n + lane < P.J)
-            for (int e = 0; e < 32 && m0 + e < P.I; ++e) lin_store<T>(P, f[e * 32 + (lane ^ e)], m0 + e, n + lane);
+        if (n + lane >= P.J) return;
+        const int rows = static_cast<int>(min(static_cast<int64_t>(32), P.I - m0));
+        const float bias = P.bias ? __ldg(P.bias + n + lane) : 0.f;
+        const T *res = P.res ? static_cast<const T *>(P.res) + m0 * P.ldr + n + lane : nullptr;
+        T *y = static_cast<T *>(P.y) + m0 * P.ldy + n + lane;
+        T *z = P.z ? static_cast<T *>(P.z) + m0 * P.ldz + n + lane : nullptr;
+        const int64_t ldy = P.ldy, ldz = P.ldz, ldr = P.ldr;
+        const int act = P.act;
+        constexpr int U = 8;   // rows whose operands are in flight together
+        for (int e = 0; e < rows; e += U) {
+            float v[U], r[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                v[u] = f[(e + u) * 32 + (lane ^ (e + u))] + bias;
+                r[u] = res && e + u < rows ? to_f32(res[u * ldr]) : 0.f;
+            }
+            if (z) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (e + u < rows) z[u * ldz] = from_f32<T>(v[u]);
+                z += U * ldz;
+            }
+            act_values(act, v);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (e + u < rows) y[u * ldy] = from_f32<T>(res ? v[u] + r[u] : v[u]);
+            y += U * ldy;
+            if (res) res += U * ldr;
+        }
     }
 };
 
@@ -614,7 +722,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
             i0 += rank * kLinRows + quad * 32;
             j0 += half * (bn / 2);
             uint4 r[4];
-            if (P.res && P.tma_out) out.fetch(r, i0 + lane, j0);
+            if (P.res && P.vec_out) out.fetch(r, i0 + lane, j0);
             if (!mbar_wait(&acc_full[b], (n >> 1) & 1, kLinTimeoutNs, abort)) break;
             tc_fence_after();
             for (int c = 0; c < bn / 2; c += 32) {
@@ -629,8 +737,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
                     if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&acc_empty[b]), 0));
                 }
                 if (i0 >= P.I || j0 + c >= P.J) continue;
-                // (a TMA store clips its rows at whole 16 bytes only)
-                if (P.tma_out && (j0 + c + 32 <= P.J || P.J % 8 == 0)) {
+                if (P.vec_out) {
                     uint4 now[4] = {r[0], r[1], r[2], r[3]};
                     if (P.res && !last) out.fetch(r, i0 + lane, j0 + c + 32);
                     out.block(acc, now, i0, j0 + c);
@@ -707,15 +814,28 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const LinFew P) {
                     acc[r][m] = fma2(make_float2(wv[r][q], wv[r][q + 1]), make_float2(xv[q], xv[q + 1]), acc[r][m]);
         }
     }
+    // sums over the lanes: at each step a lane keeps half of the values and
+    // sends the other half away, then the one value that is left goes round
+    constexpr int V = RN * MT;
+    float v[V];
 #pragma unroll
     for (int r = 0; r < RN; ++r)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            float s = acc[r][m].x + acc[r][m].y;
+        for (int m = 0; m < MT; ++m) v[m * RN + r] = acc[r][m].x + acc[r][m].y;
+    int index = 0;
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-            if (lane == 0) sums[warp][m * RN + r] = s;
+    for (int half = V / 2, o = 16; half > 0; half /= 2, o /= 2) {
+        const bool up = lane & o;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + half], o);
+            v[i] = (up ? v[i + half] : v[i]) + got;
         }
+        index += up ? half : 0;
+    }
+#pragma unroll
+    for (int o = 16 / V; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+    if ((lane & (32 / V - 1)) == 0) sums[warp][index] = v[0];
     __syncthreads();
     if (threadIdx.x < RN * MT) {
         const int m = threadIdx.x / RN, n = n0 + threadIdx.x % RN;
@@ -770,27 +890,57 @@ __device__ __forceinline__ void dz_block(const DzJob &J, int block) {
     const int c0 = (bx * 32 + lane) * 8;
     const int r1 = static_cast<int>(min(static_cast<int64_t>(J.M), (by + static_cast<int64_t>(1)) * J.slab));
     float acc[8] = {};
-    if (c0 < J.N) {
-#pragma unroll 2
-        for (int64_t r = static_cast<int64_t>(by) * J.slab + ty; r < r1; r += kDzRows) {
-            float v[8], zv[8] = {};
-            if (VEC && c0 + 8 <= J.N) {
-                Vec<T>::widen(*reinterpret_cast<const uint4 *>(g + r * J.ldg + c0), v);
-                if (z) Vec<T>::widen(*reinterpret_cast<const uint4 *>(z + r * J.ldz + c0), zv);
-            } else {
+    auto finish = [&](float (&v)[8], const float (&zv)[8], int64_t r) {
+        if (z) {
+            float s[8];
+            act_slopes(J.act, zv, s);
+            mul_to(v, s);
+        }
+        add_to(acc, v);
+        if (dz) *reinterpret_cast<uint4 *>(dz + r * J.lddz + c0) = Vec<T>::narrow(v);   // lddz = round_up(N, 8)
+    };
+    int64_t r = static_cast<int64_t>(by) * J.slab + ty;
+    if (VEC && c0 + 8 <= J.N) {
+        // the next two rows are under way while two are worked on
+        constexpr int U = 2;
+        const T *gp = g + r * J.ldg + c0, *zp = z ? z + r * J.ldz + c0 : nullptr;
+        const int64_t gs = kDzRows * J.ldg, zs = kDzRows * J.ldz;
+        uint4 gr[U] = {}, zr[U] = {}, gn[U] = {}, zn[U] = {};
+        auto load = [&](uint4 (&a)[U], uint4 (&b)[U], int64_t row) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    v[q] = c0 + q < J.N ? to_f32(g[r * J.ldg + c0 + q]) : 0.f;
-                    if (z && c0 + q < J.N) zv[q] = to_f32(z[r * J.ldz + c0 + q]);
+            for (int u = 0; u < U; ++u)
+                if (row + u * kDzRows < r1) {
+                    a[u] = *reinterpret_cast<const uint4 *>(gp + u * gs);
+                    if (z) b[u] = *reinterpret_cast<const uint4 *>(zp + u * zs);
                 }
+            gp += U * gs;
+            if (z) zp += U * zs;
+        };
+        load(gr, zr, r);
+#pragma unroll 2
+        for (; r < r1; r += U * kDzRows) {
+            load(gn, zn, r + U * kDzRows);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (r + u * kDzRows < r1) {
+                    float v[8], zv[8];
+                    Vec<T>::widen(gr[u], v);
+                    Vec<T>::widen(zr[u], zv);
+                    finish(v, zv, r + u * kDzRows);
+                }
+                gr[u] = gn[u];
+                zr[u] = zn[u];
             }
-            if (z) {
-                float s[8];
-                act_slopes(J.act, zv, s);
-                mul_to(v, s);
+        }
+    } else if (c0 < J.N) {
+        for (; r < r1; r += kDzRows) {
+            float v[8], zv[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                v[q] = c0 + q < J.N ? to_f32(g[r * J.ldg + c0 + q]) : 0.f;
+                zv[q] = z && c0 + q < J.N ? to_f32(z[r * J.ldz + c0 + q]) : 0.f;
             }
-            add_to(acc, v);
-            if (dz) *reinterpret_cast<uint4 *>(dz + r * J.lddz + c0) = Vec<T>::narrow(v);   // lddz = round_up(N, 8)
+            finish(v, zv, r);
         }
     }
     if (J.part == nullptr) return;
@@ -813,7 +963,7 @@ struct LinPrep {
     PackJob pack[2];
 };
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) linear_prep_kernel(const __grid_constant__ LinPrep P) {
+__global__ void __launch_bounds__(256, 3) linear_prep_kernel(const __grid_constant__ LinPrep P) {
     int b = blockIdx.x;
     if (b < P.dz.blocks) return dz_block<T, VEC>(P.dz, b);
     b -= P.dz.blocks;

@@ -438,8 +438,8 @@ typedef struct {
  *   z         [M][N] of `dtype`, or NULL: the pre-activation, rounded, for the
  *             backward pass.  y is computed from the unrounded z.
  *   workspace at least mqc_linear_fwd_workspace_bytes() bytes (0 when the rows
- *             of x and w are multiples of 16 bytes or M is at most 8; else their padded
- *             copies).
+ *             of x and w are multiples of 16 bytes, and for few tokens; else
+ *             their padded copies).
  * Products are exact and summed in fp32 on the tensor cores.  y and z must
  * not overlap x, w or each other.  M = 0 succeeds and writes nothing; N and K
  * are at least 1.  The strides that an absent matrix would have are ignored.
