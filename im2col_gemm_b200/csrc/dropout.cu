@@ -14,14 +14,16 @@ namespace {
 // 3", SC 2011): ten rounds of two 32 x 32 -> 64-bit products.  The 64-bit
 // variant that the stochastic quantizer uses would cost about twice the
 // instructions per random bit here, and this pass is close to issue-bound.
-__device__ __forceinline__ uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1) {
+// keys: the ten rounds' keys, advanced on the host.
+struct PhiloxKeys {
+    uint32_t k[10][2];
+};
+__device__ __forceinline__ uint4 philox4x32_10(uint4 c, const PhiloxKeys &keys) {
 #pragma unroll
     for (int r = 0; r < 10; ++r) {
         const uint64_t p = static_cast<uint64_t>(c.x) * 0xD2511F53u, q = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
-        c = make_uint4(static_cast<uint32_t>(q >> 32) ^ c.y ^ k0, static_cast<uint32_t>(q),
-                       static_cast<uint32_t>(p >> 32) ^ c.w ^ k1, static_cast<uint32_t>(p));
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
+        c = make_uint4(static_cast<uint32_t>(q >> 32) ^ c.y ^ keys.k[r][0], static_cast<uint32_t>(q),
+                       static_cast<uint32_t>(p >> 32) ^ c.w ^ keys.k[r][1], static_cast<uint32_t>(p));
     }
     return c;
 }
@@ -30,20 +32,31 @@ struct DropoutParams {
     const void *x, *res;
     void *y;
     int64_t ldx, ldr, ldy, cols, total;   // total = rows * cols
-    uint64_t seed, offset;
+    uint64_t offset;
     const uint64_t *offset_dev;
-    uint32_t drop;                        // an element stays when its 16 bits are >= drop
+    PhiloxKeys keys;
+    uint32_t bar;                         // t << 16: an element stays when its 16 bits << 16 are >= bar
+    int32_t none;                         // t = 65536: nothing stays
     float scale;
 };
 
+// Whether element e of a block stays: its half of the word, moved to the top,
+// against the bar (the low bits under it decide nothing).
+__device__ __forceinline__ bool stays(const uint32_t (&w)[4], int e, const DropoutParams &P) {
+    return ((e & 1) ? w[e / 2] : w[e / 2] << 16) >= P.bar && !P.none;
+}
+
 // A thread owns one Philox block: eight consecutive elements of the logical
-// row-major matrix.  VEC: the eight are contiguous in every tensor and start
-// at 16-byte boundaries (one long row, or rows of whole blocks); a last,
-// partial block and everything else goes element by element.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams P) {
+// row-major matrix.  Where they are contiguous in every tensor and start at
+// 16-byte boundaries (kFlat: one long row, kRows: rows of whole blocks) they
+// move as vectors; a last, partial block and everything else (kAny) goes
+// element by element.
+// Bound by memory, with the issue slots close behind (the ten rounds' products
+// fill the multiplier): 16384 x 2048 bf16 with a residual moves 201 MB.
+enum DropoutForm { kAny = 0, kRows = 1, kFlat = 2 };
+template <typename T, int FORM>
+__global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ DropoutParams P) {
     const uint64_t offset = P.offset + (P.offset_dev ? *P.offset_dev : 0);
-    const uint32_t k0 = static_cast<uint32_t>(P.seed), k1 = static_cast<uint32_t>(P.seed >> 32);
     const int64_t blocks = (P.total + 7) / 8;
     const T *x = static_cast<const T *>(P.x), *res = static_cast<const T *>(P.res);
     T *y = static_cast<T *>(P.y);
@@ -52,11 +65,11 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams P) {
          b += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int64_t i0 = b * 8;
         int64_t row = 0, col = i0;
-        if (P.cols != P.total) {
+        if (FORM != kFlat && P.cols != P.total) {
             row = P.total <= 0xFFFFFFFFll ? static_cast<uint32_t>(i0) / static_cast<uint32_t>(P.cols) : i0 / P.cols;
             col = i0 - row * P.cols;
         }
-        if (VEC && i0 + 8 <= P.total) {
+        if (FORM != kAny && i0 + 8 <= P.total) {
             uint4 xv[8 / n], rv[8 / n];
 #pragma unroll
             for (int v = 0; v < 8 / n; ++v) xv[v] = reinterpret_cast<const uint4 *>(x + row * P.ldx + col)[v];
@@ -65,23 +78,21 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams P) {
                 for (int v = 0; v < 8 / n; ++v) rv[v] = reinterpret_cast<const uint4 *>(res + row * P.ldr + col)[v];
             const uint4 r = philox4x32_10(make_uint4(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32),
                                                      static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)),
-                                          k0, k1);
+                                          P.keys);
             const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
             for (int v = 0; v < 8 / n; ++v) {
-                float f[n];
+                float f[n], scale[n];
                 Vec<T>::widen(xv[v], f);
 #pragma unroll
-                for (int q = 0; q < n; ++q) {
-                    const int e = v * n + q;
-                    const uint32_t bits = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu;
-                    f[q] = bits >= P.drop ? f[q] * P.scale : 0.f;
-                }
+                for (int q = 0; q < n; ++q) scale[q] = P.scale;
+                mul_to(f, scale);
+#pragma unroll
+                for (int q = 0; q < n; ++q) f[q] = stays(w, v * n + q, P) ? f[q] : 0.f;
                 if (res) {
                     float a[n];
                     Vec<T>::widen(rv[v], a);
-#pragma unroll
-                    for (int q = 0; q < n; ++q) f[q] += a[q];
+                    add_to(f, a);
                 }
                 reinterpret_cast<uint4 *>(y + row * P.ldy + col)[v] = Vec<T>::narrow(f);
             }
@@ -89,13 +100,12 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams P) {
         }
         const uint4 r = philox4x32_10(make_uint4(static_cast<uint32_t>(b), static_cast<uint32_t>(b >> 32),
                                                  static_cast<uint32_t>(offset), static_cast<uint32_t>(offset >> 32)),
-                                      k0, k1);
+                                      P.keys);
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (i0 + e < P.total) {
-                const uint32_t bits = (e & 1) ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu;
-                float f = bits >= P.drop ? to_f32(x[row * P.ldx + col]) * P.scale : 0.f;
+                float f = stays(w, e, P) ? to_f32(x[row * P.ldx + col]) * P.scale : 0.f;
                 if (res) f += to_f32(res[row * P.ldr + col]);
                 y[row * P.ldy + col] = from_f32<T>(f);
                 if (++col == P.cols) {
@@ -108,11 +118,12 @@ __global__ void __launch_bounds__(256) dropout_kernel(const DropoutParams P) {
 }
 
 template <typename T>
-void launch(const DropoutParams &p, bool vec, int sms, cudaStream_t s) {
+void launch(const DropoutParams &p, DropoutForm form, int sms, cudaStream_t s) {
     const int64_t blocks = std::min<int64_t>(ceil_div(ceil_div(p.total, 8), 256), int64_t(sms) * 32);
     const unsigned grid = static_cast<unsigned>(blocks);
-    if (vec) dropout_kernel<T, true><<<grid, 256, 0, s>>>(p);
-    else dropout_kernel<T, false><<<grid, 256, 0, s>>>(p);
+    if (form == kFlat) dropout_kernel<T, kFlat><<<grid, 256, 0, s>>>(p);
+    else if (form == kRows) dropout_kernel<T, kRows><<<grid, 256, 0, s>>>(p);
+    else dropout_kernel<T, kAny><<<grid, 256, 0, s>>>(p);
 }
 
 mqc_status dropout(const char *name, const void *x, int64_t ldx, const void *res, int64_t ldr, int64_t rows,
@@ -145,20 +156,26 @@ mqc_status dropout(const char *name, const void *x, int64_t ldx, const void *res
     P.ldy = ldy;
     P.cols = cols;
     P.total = rows * cols;
-    P.seed = seed;
+    for (uint32_t r = 0; r < 10; ++r) {
+        P.keys.k[r][0] = static_cast<uint32_t>(seed) + r * 0x9E3779B9u;
+        P.keys.k[r][1] = static_cast<uint32_t>(seed >> 32) + r * 0xBB67AE85u;
+    }
     P.offset = offset;
     P.offset_dev = offset_dev;
-    P.drop = static_cast<uint32_t>(std::floor(p * 65536.0 + 0.5));
-    P.scale = P.drop >= 65536u ? 0.f : 65536.f / static_cast<float>(65536u - P.drop);
+    const uint32_t t = static_cast<uint32_t>(std::floor(p * 65536.0 + 0.5));
+    P.none = t >= 65536u;
+    P.bar = P.none ? 0u : t << 16;
+    P.scale = P.none ? 0.f : 65536.f / static_cast<float>(65536u - t);
     // rows that follow one another are one long row
     const bool one = rows == 1 || (ldx == cols && ldy == cols && (!res || ldr == cols));
     if (one) P.cols = P.total;
     const int64_t per16 = 16 / dtype_bytes(dtype);
-    const bool vec = one || (cols % 8 == 0 && ldx % per16 == 0 && ldy % per16 == 0 && (!res || ldr % per16 == 0));
+    const bool rows16 = cols % 8 == 0 && ldx % per16 == 0 && ldy % per16 == 0 && (!res || ldr % per16 == 0);
+    const DropoutForm form = one ? kFlat : (rows16 ? kRows : kAny);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == MQC_F32) launch<float>(P, vec, d.sms, s);
-    else if (dtype == MQC_BF16) launch<__nv_bfloat16>(P, vec, d.sms, s);
-    else launch<__half>(P, vec, d.sms, s);
+    if (dtype == MQC_F32) launch<float>(P, form, d.sms, s);
+    else if (dtype == MQC_BF16) launch<__nv_bfloat16>(P, form, d.sms, s);
+    else launch<__half>(P, form, d.sms, s);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "dropout_kernel launch");
 }
