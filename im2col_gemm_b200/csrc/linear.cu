@@ -158,14 +158,26 @@ struct PairPlan {
     double us;
 };
 int64_t pair_tiles(const Product &p, int bn) { return ceil_div(p.tokens, 2 * kLinRows) * ceil_div(p.features, bn); }
+// How the second product's tiles make up for the first's last, partial round
+// (pair_tile): as many as weigh one of the first's, for each pair without one.
+void deal(int64_t t0, int64_t t1, int64_t kb0, int64_t kb1, int pairs, int32_t &early, int32_t &late_from) {
+    late_from = static_cast<int32_t>(t0 % pairs);
+    early = 0;
+    if (t1 > 0 && late_from > 0)
+        early = static_cast<int32_t>(std::min((kb0 + kb1 / 2) / kb1, t1 / (pairs - late_from)));
+}
 PairPlan plan_pairs(const Product *const *p, int count, int pairs) {
     PairPlan best{0, 1e300};
     for (int bn = 256; bn >= 128; bn /= 2) {
         const int64_t t0 = pair_tiles(*p[0], bn), t1 = count > 1 ? pair_tiles(*p[1], bn) : 0;
-        int64_t most = 0;   // tiles are dealt out in turn
+        const int64_t kb0 = p[0]->kblocks(), kb1 = count > 1 ? p[1]->kblocks() : 1;
+        int32_t early, late_from;
+        deal(t0, t1, kb0, kb1, pairs, early, late_from);
+        int64_t most = 0;
         for (int c = 0; c < pairs; ++c) {
-            const int64_t n0 = (t0 - c + pairs - 1) / pairs, n = (t0 + t1 - c + pairs - 1) / pairs;
-            most = std::max(most, n0 * p[0]->kblocks() + (count > 1 ? (n - n0) * p[1]->kblocks() : 0));
+            const int64_t rest = t1 - int64_t(early) * (pairs - late_from);
+            const int64_t n0 = (t0 - c + pairs - 1) / pairs, n1 = (rest - c + pairs - 1) / pairs;
+            most = std::max(most, n0 * kb0 + ((c >= late_from ? early : 0) + n1) * kb1);
         }
         const double us = 4.5 + most * (bn == 256 ? 0.40 : 0.32) + bn / 85.0;
         if (us < best.us) best = PairPlan{bn, us};
@@ -174,7 +186,7 @@ PairPlan plan_pairs(const Product *const *p, int count, int pairs) {
 }
 
 // One or two products on CTA pairs, the longer reduction's tiles first (they
-// are dealt out in turn, so the shorter ones even out the end).
+// are dealt out in turn, and the shorter ones even out the end).
 mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool bf16, const DeviceLimits &d,
                         cudaStream_t stream) {
     const int pairs = d.sms / 2;
@@ -202,6 +214,8 @@ mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool 
         if (st != MQC_OK) return st;
     }
     G.tiles = static_cast<int32_t>(tiles);
+    if (count > 1 && tiles >= pairs)
+        deal(G.first, tiles - G.first, order[0]->kblocks(), order[1]->kblocks(), pairs, G.early, G.late_from);
     return launch_group(G, true, bf16, 2 * std::min<int64_t>(tiles, pairs), 2, kPairThreads,
                         1024 + stages * stage + kPairStaging, d, stream);
 }

@@ -55,6 +55,7 @@ struct LinGroup {
     LinParams p[2];
     int32_t first;                   // tiles (single tiles: clusters) of p[0]; those of p[1] follow
     int32_t tiles;                   // of both
+    int32_t early, late_from;        // CTA pairs: see pair_tile
     int32_t cluster;                 // single tiles: CTAs of a cluster, a multiple of both products' splits
     BiasGrad bias;                   // gb NULL: none
 };
@@ -559,6 +560,29 @@ struct PairEpilogue {
     }
 };
 
+// The n-th tile of pair c of `pairs`, or -1.  The tiles of the first product
+// (the longer reduction) are dealt out in turn.  Pairs from `late_from` on got
+// one of them less; they take `early` tiles of the second product in its
+// stead, and the rest of those is dealt out in turn again.  (8192 x 2048 x
+// 2048: 64 tiles of 128 blocks, then 256 of 32 on 74 pairs; dealt out in turn
+// alone the busiest pair has 256 blocks, so 224.)
+__device__ __forceinline__ int pair_tile(const LinGroup &G, int c, int pairs, int n) {
+    const int own = G.first > c ? (G.first - c - 1) / pairs + 1 : 0;
+    if (n < own) return c + n * pairs;
+    n -= own;
+    int at = G.first;
+    if (G.early > 0) {
+        const int late = pairs - G.late_from;
+        if (c >= G.late_from) {
+            if (n < G.early) return at + (c - G.late_from) + n * late;
+            n -= G.early;
+        }
+        at += G.early * late;
+    }
+    at += c + n * pairs;
+    return at < G.tiles ? at : -1;
+}
+
 // Large products: a persistent pair of CTAs (one per SM) computes 256 x bn
 // tiles with tcgen05.mma.cta_group::2.  Each CTA holds 128 rows of A and half
 // of B's rows per stage, so an SM reads half the operand bytes from shared
@@ -580,7 +604,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
     // the same for both products
     const int bn = G.p[0].bn, b_bytes = G.p[0].b_bytes, stages = G.p[0].stages;
     const int stage_bytes = a_bytes + b_bytes;
-    const int step = gridDim.x / 2;
+    const int pairs = gridDim.x / 2, me = blockIdx.x / 2;
     volatile int *abort = &abort_flag;
 
     if (warp == 0 && lane == 0) {
@@ -626,7 +650,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
         const bool issuer = elect_one();
         int s = 0, ph = 0, issued = 0;
         bool ok = true;
-        for (int t = blockIdx.x / 2; t < G.tiles && ok; t += step) {
+        for (int n = 0, t; ok && (t = pair_tile(G, me, pairs, n)) >= 0; ++n) {
             int i0, j0;
             const LinParams &P = place(t, i0, j0);
             const int nkb = (P.R + kLinBK - 1) / kLinBK;
@@ -671,9 +695,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
         }
     } else if (warp == 1 && rank == 0) {
         const bool issuer = elect_one();
-        int s = 0, ph = 0, n = 0;
+        int s = 0, ph = 0;
         bool ok = true;
-        for (int t = blockIdx.x / 2; t < G.tiles && ok; t += step, ++n) {
+        for (int n = 0, t; ok && (t = pair_tile(G, me, pairs, n)) >= 0; ++n) {
             const LinParams &P = G.p[t >= G.first];
             const int nkb = (P.R + kLinBK - 1) / kLinBK;
             const uint32_t a_step = P.a_mn ? 2048 : 32, b_step = P.b_mn ? 2048 : 32;
@@ -709,12 +733,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
     } else if (warp == 1) {
         // the second CTA's: the bias gradient
         if (G.bias.gb)
-            for (int c = blockIdx.x / 2 * 32 + lane; c < G.bias.N; c += step * 32) bias_grad_column(G.bias, c);
+            for (int c = me * 32 + lane; c < G.bias.N; c += pairs * 32) bias_grad_column(G.bias, c);
     } else {
         // warps 2-9: a quadrant of the rows, half of the columns
         const int quad = warp & 3, half = (warp - 2) / 4;
-        int n = 0, turn = 0;
-        for (int t = blockIdx.x / 2; t < G.tiles; t += step, ++n) {
+        int turn = 0;
+        for (int n = 0, t; (t = pair_tile(G, me, pairs, n)) >= 0; ++n) {
             const int b = n & 1;
             int i0, j0;
             const LinParams &P = place(t, i0, j0);
