@@ -11,7 +11,8 @@
 namespace mqc {
 namespace {
 
-mqc_status check_tensor(const char *name, const char *what, const void *p, const mqc_t4 *d, const mqc_t4 *like) {
+mqc_status check_tensor(const char *name, const char *what, const void *p, const mqc_t4 *d, const mqc_t4 *like,
+                        bool written) {
     if (p == nullptr || d == nullptr) return fail(MQC_ERR_INVALID, "%s: %s or its descriptor is null", name, what);
     if (d->d0 != like->d0 || d->d1 != like->d1 || d->d2 != like->d2 || d->d3 != like->d3)
         return fail(MQC_ERR_INVALID, "%s: the extents of %s differ", name, what);
@@ -23,6 +24,18 @@ mqc_status check_tensor(const char *name, const char *what, const void *p, const
                     name, what);
     if (((many_w || many_h) && sp < d->d1) || sp > (int64_t(1) << 38) || d->s0 < 0 || d->s0 > (int64_t(1) << 44))
         return fail(MQC_ERR_UNSUPPORTED, "%s: strides of %s out of range", name, what);
+    // images one after another, or interleaved pixel by pixel
+    const int64_t pixels = (int64_t(d->d2) * d->d3 - 1) * sp + d->d1, images = int64_t(d->d0 - 1) * d->s0 + d->d1;
+    if (written && d->d0 > 1 && d->s0 < pixels && !(d->s0 >= d->d1 && sp >= images))
+        return fail(MQC_ERR_UNSUPPORTED, "%s: the images of %s overlap", name, what);
+    return MQC_OK;
+}
+
+// fp32 parameters and statistics, NULL allowed.
+mqc_status check_params(const char *name, const float *const *p, int count) {
+    for (int i = 0; i < count; ++i)
+        if ((reinterpret_cast<uintptr_t>(p[i]) & 3u) != 0)
+            return fail(MQC_ERR_ALIGNMENT, "%s: parameters and statistics must be 4-byte aligned", name);
     return MQC_OK;
 }
 
@@ -175,8 +188,8 @@ int plan_passes(GnParams &P, int vec, int32_t dtype) {
         P.chunks = P.G * P.pieces;
     } else {
         P.gpc = unit;
-        for (int g = unit; g <= P.G; g += unit)
-            if (P.G % g == 0 && int64_t(g) * P.D * dtype_bytes(dtype) <= 512) P.gpc = g;
+        for (int g = unit; g <= P.G && int64_t(g) * P.D * dtype_bytes(dtype) <= 512; g += unit)
+            if (P.G % g == 0) P.gpc = g;
         P.pieces = 1;
         P.width = P.gpc * P.D;
         P.chunks = P.G / P.gpc;
@@ -363,9 +376,11 @@ mqc_status mqc_group_norm_fwd(const void *x, const mqc_t4 *xd, int32_t dtype, co
     if (st != MQC_OK) return st;
     if (!(eps >= 0.f)) return fail(MQC_ERR_INVALID, "%s: eps must not be negative", name);
     if (xd->d0 == 0) return MQC_OK;
-    if ((st = check_tensor(name, "x", x, xd, xd)) != MQC_OK) return st;
-    if ((st = check_tensor(name, "y", y, yd, xd)) != MQC_OK) return st;
+    if ((st = check_tensor(name, "x", x, xd, xd, false)) != MQC_OK) return st;
+    if ((st = check_tensor(name, "y", y, yd, xd, true)) != MQC_OK) return st;
     if (mean == nullptr || rstd == nullptr) return fail(MQC_ERR_INVALID, "%s: null statistics", name);
+    const float *params[4] = {gamma, beta, mean, rstd};
+    if ((st = check_params(name, params, 4)) != MQC_OK) return st;
     GnParams P{};
     fill(P, xd, groups);
     const mqc_t4 *all[2] = {xd, yd};
@@ -394,15 +409,17 @@ mqc_status mqc_group_norm_bwd(const void *g, const mqc_t4 *gd, const void *x, co
     mqc_status st = check_extents(name, xd, dtype, groups, act);
     if (st != MQC_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const float *params[6] = {gamma, beta, mean, rstd, ggamma, gbeta};
+    if ((st = check_params(name, params, 6)) != MQC_OK) return st;
     if (xd->d0 == 0) {
         cudaError_t e = cudaSuccess;
         if (ggamma) e = cudaMemsetAsync(ggamma, 0, size_t(xd->d1) * 4, s);
         if (e == cudaSuccess && gbeta) e = cudaMemsetAsync(gbeta, 0, size_t(xd->d1) * 4, s);
         return e == cudaSuccess ? MQC_OK : cuda_fail(e, "group_norm_bwd memset");
     }
-    if ((st = check_tensor(name, "x", x, xd, xd)) != MQC_OK) return st;
-    if ((st = check_tensor(name, "g", g, gd, xd)) != MQC_OK) return st;
-    if ((st = check_tensor(name, "gx", gx, gxd, xd)) != MQC_OK) return st;
+    if ((st = check_tensor(name, "x", x, xd, xd, false)) != MQC_OK) return st;
+    if ((st = check_tensor(name, "g", g, gd, xd, false)) != MQC_OK) return st;
+    if ((st = check_tensor(name, "gx", gx, gxd, xd, true)) != MQC_OK) return st;
     if (mean == nullptr || rstd == nullptr) return fail(MQC_ERR_INVALID, "%s: null statistics", name);
     GnParams P{};
     fill(P, xd, groups);

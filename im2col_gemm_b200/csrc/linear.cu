@@ -347,6 +347,9 @@ void launch_few(const LinFew &P, cudaStream_t s) {
 mqc_status check_linear(const mqc_linear *l, const char *name) {
     if (l == nullptr) return fail(MQC_ERR_INVALID, "%s: null descriptor", name);
     if (l->M < 0 || l->N <= 0 || l->K <= 0) return fail(MQC_ERR_INVALID, "%s: bad extents", name);
+    // row numbers and byte offsets in a row stay within 31 bits
+    if (l->M > (1 << 30) || l->N > (1 << 29) || l->K > (1 << 29))
+        return fail(MQC_ERR_INVALID, "%s: M above 2^30, or N or K above 2^29", name);
     if (!act_ok(l->act)) return fail(MQC_ERR_INVALID, "%s: bad activation", name);
     if (l->dtype == MQC_F32)
         return fail(MQC_ERR_UNSUPPORTED, "%s: fp32 operands (the tensor cores take bf16 or fp16)", name);

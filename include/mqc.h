@@ -382,7 +382,8 @@ typedef enum { MQC_F32 = 0, MQC_BF16 = 1, MQC_F16 = 2 } mqc_dtype;
  *   x, y    [N][C][H][W] tensors of `dtype`, described by xd and yd (d0 = N,
  *           d1 = C, d2 = H, d3 = W) in elements: element stride 1 along the
  *           channels, and rows of pixels that follow one another (s2 = d3 *
- *           s3, any s3 >= C; any s0), else MQC_ERR_UNSUPPORTED.  y may be x
+ *           s3, any s3 >= C; any s0, as long as the images of an output do not
+ *           overlap), else MQC_ERR_UNSUPPORTED.  y may be x
  *           itself (same descriptor); partial overlap is not allowed.
  *   gamma, beta   fp32 [C]; NULL stands for ones / zeros.
  *   groups  divides C.      eps >= 0.     act  MQC_ACT_*, GELU included.
@@ -422,7 +423,7 @@ MQC_API size_t mqc_group_norm_bwd_workspace_bytes(const mqc_t4 *gd, const mqc_t4
 
 /* One linear layer: M rows (tokens, pixels) of K features to N features.
  * Every matrix is row-major with its own row stride in elements (at least
- * its number of columns); `dtype` is MQC_BF16 or MQC_F16 (MQC_F32 is
+ * its number of columns); M is at most 2^30, N and K 2^29.  `dtype` is MQC_BF16 or MQC_F16 (MQC_F32 is
  * MQC_ERR_UNSUPPORTED: the tensor cores have no fp32 operands). */
 typedef struct {
     int32_t M, N, K;

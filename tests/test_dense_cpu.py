@@ -92,6 +92,8 @@ def test_linear_refusals(mqc):
         l, x, w, b, r, y, z, ws, n, None)
     assert fwd(lin(M=0)) == 0                       # nothing to write
     assert fwd(lin(M=-1)) == -1 and fwd(lin(N=0)) == -1 and fwd(lin(K=0)) == -1
+    assert fwd(lin(M=(1 << 30) + 1)) == -1 and fwd(lin(N=(1 << 29) + 1, ldy=1 << 30)) == -1
+    assert fwd(lin(K=(1 << 29) + 1, ldx=1 << 30, ldw=1 << 30)) == -1
     assert fwd(lin(act=4)) == -1 and fwd(lin(act=-1)) == -1
     assert fwd(lin(dtype=0)) == -2 and fwd(lin(dtype=3)) == -1
     assert "fp32" in (fwd(lin(dtype=0)), mqc.lib.mqc_last_error_message().decode())[1]
@@ -145,6 +147,10 @@ def test_group_norm_refusals(mqc):
     assert fwd(wide(), dtype=0, ws=ODD) == -5
     need = mqc.mqc_group_norm_bwd_workspace_bytes(d(), d(), d(), 1, 4)
     assert need > 0
+
+    assert fwd(yd=d(s=(0, 1, 40, 8))) == -2 and "overlap" in mqc.lib.mqc_last_error_message().decode()
+    assert fwd(yd=d(s=(112, 1, 40, 8))) == -2        # an image ends inside the next
+    assert fwd(mean=ctypes.c_void_p(258)) == -5 and fwd(rstd=ctypes.c_void_p(257)) == -5
 
     def bwd(gd=None, g=P16, x=P16, gx=P16, mean=P16, rstd=P16, groups=4, a=0, ws=P16, n=1 << 20):
         return mqc.mqc_group_norm_bwd(g, gd or d(), x, d(), 1, None, None, mean, rstd, groups, a, gx, d(), P16, P16,

@@ -55,7 +55,8 @@ SHAPES = [  # (N, C, H, W, groups)
     (1, 1, 1, 1, 1), (1, 8, 1, 1, 2), (3, 7, 1, 1, 7), (2, 30, 5, 7, 3), (1, 256, 14, 14, 32), (2, 64, 9, 8, 8),
     (2, 320, 20, 20, 32), (1, 33, 17, 3, 11), (5, 12, 64, 1, 4), (1, 16, 1, 1000, 1), (4, 2048, 3, 3, 32),
     (2, 4104, 4, 4, 8), (1, 16, 200, 200, 4), (40, 24, 6, 6, 24), (1, 514, 31, 33, 2), (300, 16, 3, 3, 4),
-    (2, 1024, 40, 40, 32), (1, 96, 160, 160, 32),
+    (2, 1024, 40, 40, 32), (1, 96, 160, 160, 32), (1, 4096, 9, 9, 1), (3, 2051, 7, 5, 1), (4, 64, 160, 160, 16),
+    (1, 924, 53, 88, 4), (6, 34, 64, 64, 2),
 ]
 
 
@@ -155,7 +156,23 @@ def test_strides_and_untouched_gaps(mqc, shape, gap_c, gap_n, dtype):
         assert (whole == 5.0).all()
 
 
-@pytest.mark.parametrize("shape", [(2, 32, 8, 8, 4), (1, 96, 160, 160, 32)])
+@pytest.mark.parametrize("shape", [(3, 16, 5, 6, 4), (4, 64, 160, 160, 16)])
+def test_interleaved_images(mqc, shape):
+    """[H][W][N][C] tensors: the images' pixels alternate in memory."""
+    n, c, h, w, groups = shape
+    t = make(n, c, h, w, BF16)
+    mix = lambda v: v.permute(2, 3, 0, 1).contiguous().permute(2, 3, 0, 1)  # noqa: E731
+    y0, mean, rstd = mqc.group_norm_fwd(t["x"], groups, t["gamma"], t["beta"], EPS, 2)
+    x = mix(t["x"])
+    y1 = mqc.group_norm_fwd(x, groups, t["gamma"], t["beta"], EPS, 2, out=torch.empty_like(x))[0]
+    assert x.stride()[0] == c and torch.equal(y0, y1)
+    a = mqc.group_norm_bwd(t["g"], t["x"], groups, mean, rstd, t["gamma"], t["beta"], 2)
+    b = mqc.group_norm_bwd(mix(t["g"]), x, groups, mean, rstd, t["gamma"], t["beta"], 2, out=torch.empty_like(x))
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("shape", [(2, 32, 8, 8, 4), (1, 96, 160, 160, 32), (4, 64, 160, 160, 16)])
 def test_in_place(mqc, shape):
     *dims, groups = shape
     t = make(*dims, BF16)
@@ -178,7 +195,8 @@ def test_empty_batch(mqc):
     assert gx.shape == x.shape and not ggamma.any() and not gbeta.any()
 
 
-@pytest.mark.parametrize("shape", [(1, 64, 14, 14, 8), (2, 96, 100, 90, 32), (130, 40, 14, 14, 8)])
+@pytest.mark.parametrize("shape", [(1, 64, 14, 14, 8), (2, 96, 100, 90, 32), (130, 40, 14, 14, 8),
+                                   (4, 64, 160, 160, 16), (3, 602, 60, 17, 2)])
 def test_same_bits_each_time(mqc, shape):
     *dims, groups = shape
     t = make(*dims, BF16)
