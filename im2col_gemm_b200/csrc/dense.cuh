@@ -155,8 +155,8 @@ struct Silu {
 // The same with one reciprocal for two elements, of the product of their
 // denominators, where exponentials and reciprocals (an eighth of the rate of
 // other arithmetic) bound a pass; an element's last bits then depend on its
-// neighbour.  Denominators stop at 2^62, so that their product is finite;
-// below z = -43, where sigmoid is under 2^-62, it is given as 0.
+// neighbour.  Denominators stop at 2^62, so that their product is finite:
+// sigmoid is at least 2^-62 then, too much by that below z = -43.
 struct SiluPair {
     __device__ static __forceinline__ float2 sigmoid(float2 z) {
         float2 t = mul2(z, both(-1.4426950408889634f));
@@ -164,8 +164,7 @@ struct SiluPair {
         const float2 d = add2(exp2_2(t), both(1.f));
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
-        const float2 q = mul2(make_float2(d.y, d.x), both(r));
-        return make_float2(t.x < 62.f ? q.x : z.x * 0.f, t.y < 62.f ? q.y : z.y * 0.f);
+        return mul2(make_float2(d.y, d.x), both(r));
     }
     __device__ static __forceinline__ float2 value(float2 z) { return mul2(z, sigmoid(z)); }
     __device__ static __forceinline__ float2 slope(float2 z) { return Silu::slope_of(z, sigmoid(z)); }
