@@ -547,10 +547,20 @@ def _scratch(nbytes: int, like, workspace):
     if workspace is None:
         if nbytes == 0:
             return None, None, 0
-        torch = _torch()
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        workspace = like.new_empty(nbytes, dtype=_torch().uint8)
         return workspace, workspace.data_ptr(), nbytes
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _image_like(x, xd: T4, out) -> tuple:
+    """(tensor, descriptor) of an output beside x: `out`, or a new channels-last tensor."""
+    if out is not None:
+        return out, _image_desc(out, x.shape)
+    torch = _torch()
+    if x.is_contiguous(memory_format=torch.channels_last):
+        return torch.empty_like(x), xd
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device, memory_format=torch.channels_last)
+    return y, T4(*x.shape, *y.stride())
 
 
 def _image_desc(t, shape) -> T4:
@@ -565,16 +575,14 @@ def group_norm_fwd(x, groups: int, gamma=None, beta=None, eps: float = 1e-5, act
     """act(group norm of x) for a channels-last tensor x [N][C][H][W] (torch's
     channels_last strides, or any pixel and image strides): (y, mean, rstd),
     mean and rstd fp32 [N][groups] for the backward pass."""
-    torch, shape, dt = _torch(), x.shape, _dtype(x)
+    shape, dt = x.shape, _dtype(x)
     if len(shape) != 4:
         raise ValueError("group_norm_fwd takes [N][C][H][W] tensors")
     _same(x, out)
     _params(x, shape[1], gamma, beta)
     xd = _image_desc(x, shape)
-    y = out if out is not None else torch.empty(shape, dtype=x.dtype, device=x.device,
-                                                memory_format=torch.channels_last)
-    yd = _image_desc(y, shape)
-    mean, rstd = torch.empty((2, shape[0], max(groups, 0)), dtype=torch.float32, device=x.device).unbind(0)
+    y, yd = _image_like(x, xd, out)
+    mean, rstd = x.new_empty((2, shape[0], max(groups, 0)), dtype=torch.float32).unbind(0)
     ws, at, nws = _scratch(lib.mqc_group_norm_fwd_workspace_bytes(xd, yd, dt, groups), x, workspace)
     check(lib.mqc_group_norm_fwd(x.data_ptr(), xd, dt, _address(gamma), _address(beta), groups, eps, act, y.data_ptr(),
                                  yd, mean.data_ptr(), rstd.data_ptr(), at, nws, _CUDA["stream"](x.get_device())))
@@ -585,17 +593,15 @@ def group_norm_fwd(x, groups: int, gamma=None, beta=None, eps: float = 1e-5, act
 def group_norm_bwd(g, x, groups: int, mean, rstd, gamma=None, beta=None, act: int = ACT_NONE, out=None,
                    workspace=None):
     """Gradients of group_norm_fwd: (gx, ggamma, gbeta), the last two fp32 [C]."""
-    torch, shape, dt = _torch(), x.shape, _dtype(x)
+    shape, dt = x.shape, _dtype(x)
     if len(shape) != 4:
         raise ValueError("group_norm_bwd takes [N][C][H][W] tensors")
     _same(g, x, out)
     _params(x, shape[1], gamma, beta)
     _params(x, shape[0] * groups, mean, rstd)
     gd, xd = _image_desc(g, shape), _image_desc(x, shape)
-    gx = out if out is not None else torch.empty(shape, dtype=x.dtype, device=x.device,
-                                                 memory_format=torch.channels_last)
-    gxd = _image_desc(gx, shape)
-    ggamma, gbeta = torch.empty((2, shape[1]), dtype=torch.float32, device=x.device).unbind(0)
+    gx, gxd = _image_like(x, xd, out)
+    ggamma, gbeta = x.new_empty((2, shape[1]), dtype=torch.float32).unbind(0)
     ws, at, nws = _scratch(lib.mqc_group_norm_bwd_workspace_bytes(gd, xd, gxd, dt, groups), x, workspace)
     check(lib.mqc_group_norm_bwd(g.data_ptr(), gd, x.data_ptr(), xd, dt, _address(gamma), _address(beta),
                                  mean.data_ptr(), rstd.data_ptr(), groups, act, gx.data_ptr(), gxd, ggamma.data_ptr(),
@@ -626,12 +632,11 @@ def linear_fwd(x, w, bias=None, act: int = ACT_NONE, residual=None, save_z: bool
     """(y, z): y = act(x . w^T + bias) + residual for x [M][K] and w [N][K] in
     bf16 or fp16 (rows of any stride), bias fp32 [N]; z, the pre-activation for
     the backward pass, with `save_z`, else None."""
-    torch = _torch()
     m, n, k = _linear_sizes("linear_fwd", x, w)
     _same(x, w, residual, out)
     _params(x, n, bias)
-    y = out if out is not None else torch.empty((m, n), dtype=x.dtype, device=x.device)
-    z = torch.empty((m, n), dtype=x.dtype, device=x.device) if save_z else None
+    y = out if out is not None else x.new_empty((m, n))
+    z = x.new_empty((m, n)) if save_z else None
     lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, m, k), _row_stride(w, n, k), _row_stride(residual, m, n),
                  _row_stride(out, m, n), n, n, k, k)
     ws, at, nws = _scratch(lib.mqc_linear_fwd_workspace_bytes(lin), x, workspace)
@@ -646,12 +651,11 @@ def linear_bwd(g, x, w, z=None, act: int = ACT_NONE, need_x: bool = True, need_w
     """(gx, gw, gb) of linear_fwd for the incoming gradient g [M][N]; z as the
     forward pass saved it (not read for ACT_NONE).  What is not needed is
     None."""
-    torch = _torch()
     m, n, k = _linear_sizes("linear_bwd", x, w)
     _same(g, x, w, z)
-    gx = torch.empty((m, k), dtype=x.dtype, device=x.device) if need_x else None
-    gw = torch.empty((n, k), dtype=x.dtype, device=x.device) if need_w else None
-    gb = torch.empty(n, dtype=torch.float32, device=x.device) if need_bias else None
+    gx = x.new_empty((m, k)) if need_x else None
+    gw = x.new_empty((n, k)) if need_w else None
+    gb = x.new_empty(n, dtype=torch.float32) if need_bias else None
     lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, m, k), _row_stride(w, n, k), n, n, _row_stride(z, m, n),
                  _row_stride(g, m, n), k, k)
     ws, at, nws = _scratch(lib.mqc_linear_bwd_workspace_bytes(lin), x, workspace)
@@ -691,7 +695,7 @@ def dropout_fwd(x, p: float, seed: int, offset: int = 0, residual=None, offset_d
     _dropout_check(x, residual, offset_dev)
     if out is not None:
         _dropout_check(x, out, None)
-    y = out if out is not None else _torch().empty(x.shape, dtype=x.dtype, device=x.device)
+    y = out if out is not None else x.new_empty(x.shape)
     rows, cols, (ldx, ldr, ldy) = _dropout_rows(x, residual, y)
     check(lib.mqc_dropout_fwd(x.data_ptr(), ldx, _address(residual), ldr, rows, cols, _dtype(x), p, seed, offset,
                               _address(offset_dev), y.data_ptr(), ldy, _CUDA["stream"](x.get_device())))
@@ -703,7 +707,7 @@ def dropout_bwd(g, p: float, seed: int, offset: int = 0, offset_dev=None, out=No
     """Gradient of dropout_fwd by x, with the forward call's p, seed and offset."""
     _same(g, out)
     _dropout_check(g, out, offset_dev)
-    gx = out if out is not None else _torch().empty(g.shape, dtype=g.dtype, device=g.device)
+    gx = out if out is not None else g.new_empty(g.shape)
     rows, cols, (ldg, ldgx) = _dropout_rows(g, gx)
     check(lib.mqc_dropout_bwd(g.data_ptr(), ldg, rows, cols, _dtype(g), p, seed, offset, _address(offset_dev),
                               gx.data_ptr(), ldgx, _CUDA["stream"](g.get_device())))
