@@ -286,13 +286,15 @@ mqc_status launch(GnParams &P, const GnPlan &plan, const DeviceLimits &d, cudaSt
     const size_t nt = size_t(P.tx) * P.ty, groups = 2 * size_t(P.gpc) * 4;
     if constexpr (BWD) {
         P.channel_blocks = channel_blocks;
+        const size_t ring = GnRing<T, VEC, 2>::kSlotBytes;
         const size_t sums = 4 * (2 * nt * VEC + 2 * P.threads + 2 * size_t(P.tx) * VEC);
         const size_t join = P.threads / 32 * 2 * 32 * 8;
-        gn_bwd_sums_kernel<T, VEC, UNI><<<grid, P.threads, sums, s>>>(P);
-        gn_bwd_apply_kernel<T, VEC, UNI><<<grid + channel_blocks, P.threads, std::max(groups, join), s>>>(P);
+        gn_bwd_sums_kernel<T, VEC, UNI><<<grid, P.threads, std::max(ring, sums), s>>>(P);
+        gn_bwd_apply_kernel<T, VEC, UNI><<<grid + channel_blocks, P.threads, std::max(ring + groups, join), s>>>(P);
     } else {
-        gn_stats_kernel<T, VEC, UNI><<<grid, P.threads, 4 * nt * (UNI ? 1 : P.seg) + groups, s>>>(P);
-        gn_apply_kernel<T, VEC, UNI><<<grid, P.threads, groups, s>>>(P);
+        const size_t ring = GnRing<T, VEC, 1>::kSlotBytes;
+        gn_stats_kernel<T, VEC, UNI><<<grid, P.threads, std::max(ring, 4 * nt * (UNI ? 1 : P.seg) + groups), s>>>(P);
+        gn_apply_kernel<T, VEC, UNI><<<grid, P.threads, ring + groups, s>>>(P);
     }
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "group norm launch");

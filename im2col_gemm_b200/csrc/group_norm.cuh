@@ -322,52 +322,94 @@ struct GnPlace {
     }
 };
 
+template <int BYTES>
+__device__ __forceinline__ void gn_copy_async(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void gn_copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's reads of its vectors of NT tensors, kRing of them under way: they
+// land in its own slots of shared memory ([slot][tensor][thread]), so the depth
+// costs no registers and the order needs no barrier.  (Batches loaded ahead
+// into registers: 16x64x160x160 bf16 forward took 38.9 us, now 34.7, and
+// 16x128x80x80 fp32 backward 100.6, now 88.7.)  Elements of two
+// bytes, too small for asynchronous copies, are loaded when they are due.
+template <typename T, int VEC, int NT>
+struct GnRing {
+    static constexpr int kBytes = VEC * sizeof(T);
+    static constexpr int kRing = kBytes * NT <= 16 ? 8 : 4;
+    static constexpr bool kAsync = kBytes >= 4;
+    using V = Pack<T, VEC>;
+    const T *due[NT], *ahead[NT];        // the next vector to be taken, to be asked for
+    int64_t step[NT];
+    uint8_t *slots;
+    int count;
+
+    static constexpr int kSlotBytes = kAsync ? kRing * NT * kPassThreads * kBytes : 0;
+    __device__ __forceinline__ GnRing(uint8_t *smem, int n) : slots(smem + threadIdx.x * kBytes), count(n) {}
+    __device__ __forceinline__ void ask(int i) {
+        if (!kAsync) return;
+        if (i < count) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                gn_copy_async<kBytes < 4 ? 4 : kBytes>(
+                    smem_u32(slots + ((i & (kRing - 1)) * NT + t) * kPassThreads * kBytes), ahead[t]);
+                ahead[t] += step[t];
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void begin() {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) ahead[t] = due[t];
+#pragma unroll
+        for (int i = 0; i < kRing; ++i) ask(i);
+    }
+    // The i-th vectors, and the request for those that take their place.
+    __device__ __forceinline__ void take(int i, typename V::Raw (&r)[NT]) {
+        if (kAsync) gn_copy_wait<kRing - 1>();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            if (kAsync) {
+                r[t] = V::load(reinterpret_cast<const T *>(slots + ((i & (kRing - 1)) * NT + t) * kPassThreads * kBytes));
+            } else {
+                r[t] = V::load(due[t]);
+                due[t] += step[t];
+            }
+        }
+        ask(i + kRing);
+    }
+};
+
 // First pass: mean and squared deviations of each group (or piece) of the slab.
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_stats_kernel(const __grid_constant__ GnParams P) {
-    extern __shared__ __align__(16) float gn_red[];
+    extern __shared__ __align__(16) uint8_t gn_smem[];
     using V = Pack<T, VEC>;
     const GnPlace<VEC> at(P, blockIdx.x);
+    using Ring = GnRing<T, VEC, 1>;
+    Ring ring(gn_smem, at.count);
+    ring.due[0] = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
+    ring.step[0] = P.ty * P.x.sp;
+    ring.begin();
     GnRunning<VEC> run;
-    {
-        const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
-        const int64_t step = P.ty * P.x.sp;
-        constexpr int U = 4;
-        int i = 0;
-        if (at.count > 0) {
-            float v[VEC];
-            V::widen(V::load(x), v);
-            run.start(v);
-        }
-        // the next batch is under way while one is summed
-        typename V::Raw r[U];
-        if (at.count >= U) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) r[u] = V::load(x + u * step);
-        }
-#pragma unroll 2
-        for (; i + U <= at.count; i += U) {
-            typename V::Raw next[U];
-            x += U * step;
-            if (i + 2 * U <= at.count) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) next[u] = V::load(x + u * step);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float v[VEC];
-                V::widen(r[u], v);
-                run.add(v);
-                r[u] = next[u];
-            }
-        }
-#pragma unroll 1
-        for (; i < at.count; ++i, x += step) {
-            float v[VEC];
-            V::widen(V::load(x), v);
-            run.add(v);
-        }
+#pragma unroll 4
+    for (int i = 0; i < at.count; ++i) {
+        typename V::Raw r[1];
+        ring.take(i, r);
+        float v[VEC];
+        V::widen(r[0], v);
+        if (i == 0) run.start(v);
+        run.add(v);
     }
+    __syncthreads();   // the sums take the slots' place
+    float *gn_red = reinterpret_cast<float *>(gn_smem);
     run.finish(at.count);
     const int nt = P.tx * P.ty, seg = UNI ? 1 : P.seg;
     float *mean = gn_red + nt * seg;
@@ -410,19 +452,17 @@ __device__ __forceinline__ void each_part(const GnParams &P, const GnPlace<VEC> 
 // L2.  The first loads are under way while the statistics are joined.
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_apply_kernel(const __grid_constant__ GnParams P) {
-    extern __shared__ __align__(16) float gn_red[];
+    extern __shared__ __align__(16) uint8_t gn_smem[];
     using V = Pack<T, VEC>;
+    using Ring = GnRing<T, VEC, 1>;
     const GnPlace<VEC> at(P, gridDim.x - 1 - blockIdx.x);
-    float *mean = gn_red, *rstd = gn_red + P.gpc;
-    const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
+    float *mean = reinterpret_cast<float *>(gn_smem + Ring::kSlotBytes), *rstd = mean + P.gpc;
+    Ring ring(gn_smem, at.count);
+    ring.due[0] = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
+    ring.step[0] = P.ty * P.x.sp;
+    ring.begin();
     T *y = static_cast<T *>(P.out) + at.n * P.on + at.c + at.p0 * P.op;
-    const int64_t xstep = P.ty * P.x.sp, ystep = P.ty * P.op;
-    constexpr int U = 2;
-    typename V::Raw r[U];
-    if (at.count >= U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) r[u] = V::load(x + u * xstep);
-    }
+    const int64_t ystep = P.ty * P.op;
     float a[VEC], b[VEC], m[VEC];
 #pragma unroll
     for (int q = 0; q < VEC; ++q) {
@@ -451,32 +491,17 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_apply_kernel(const __grid_
         m[q] = -mean[g];
         a[q] *= rstd[g];
     });
-    auto one = [&](const typename V::Raw &raw, T *to) {
+#pragma unroll 2
+    for (int i = 0; i < at.count; ++i, y += ystep) {
+        typename V::Raw r[1];
+        ring.take(i, r);
         float v[VEC];
-        V::widen(raw, v);
+        V::widen(r[0], v);
         add_to(v, m);
         fma_to(v, v, a, b);
         act_values<true>(P.act, v);
-        V::store(to, v);
-    };
-    int i = 0;
-#pragma unroll 2
-    for (; i + U <= at.count; i += U) {
-        typename V::Raw next[U];
-        x += U * xstep;
-        if (i + 2 * U <= at.count) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) next[u] = V::load(x + u * xstep);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            one(r[u], y + u * ystep);
-            r[u] = next[u];
-        }
-        y += U * ystep;
+        V::store(y, v);
     }
-#pragma unroll 1
-    for (; i < at.count; ++i, x += xstep, y += ystep) one(V::load(x), y);
 }
 
 // What the backward pass keeps of a thread's channels.
@@ -507,56 +532,32 @@ struct GnSlope {
 // First pass: sums of dz and dz xhat, by channel and (times gamma) by group.
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_sums_kernel(const __grid_constant__ GnParams P) {
-    extern __shared__ __align__(16) float gn_red[];
+    extern __shared__ __align__(16) uint8_t gn_smem[];
     using V = Pack<T, VEC>;
+    using Ring = GnRing<T, VEC, 2>;
     const GnPlace<VEC> at(P, blockIdx.x);
-    const int group0 = at.group(P, 0);
+    Ring ring(gn_smem, at.count);
+    ring.due[0] = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
+    ring.due[1] = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c + at.p0 * P.g.sp;
+    ring.step[0] = P.ty * P.x.sp;
+    ring.step[1] = P.ty * P.g.sp;
+    ring.begin();
     GnSlope<VEC> K;
-    K.template load<UNI>(P, at.n, group0, at.col * VEC, at.c, at.on);
+    K.template load<UNI>(P, at.n, at.group(P, 0), at.col * VEC, at.c, at.on);
     float sa[VEC] = {}, sb[VEC] = {};
-    {
-        const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
-        const T *g = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c + at.p0 * P.g.sp;
-        const int64_t xstep = P.ty * P.x.sp, gstep = P.ty * P.g.sp;
-        constexpr int U = 2;
-        auto one = [&](const typename V::Raw &rx, const typename V::Raw &rg) {
-            float xv[VEC], gv[VEC];
-            V::widen(rx, xv);
-            V::widen(rg, gv);
-            K.apply(P.act, xv, gv);
-            add_to(sa, gv);
-            fma_to(sb, gv, xv, sb);
-        };
-        int i = 0;
-        typename V::Raw rx[U], rg[U];
-        if (at.count >= U) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                rx[u] = V::load(x + u * xstep);
-                rg[u] = V::load(g + u * gstep);
-            }
-        }
 #pragma unroll 2
-        for (; i + U <= at.count; i += U) {
-            typename V::Raw nx[U], ng[U];
-            x += U * xstep;
-            g += U * gstep;
-            if (i + 2 * U <= at.count) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    nx[u] = V::load(x + u * xstep);
-                    ng[u] = V::load(g + u * gstep);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                one(rx[u], rg[u]);
-                rx[u] = nx[u];
-                rg[u] = ng[u];
-            }
-        }
-        if (i < at.count) one(V::load(x), V::load(g));
+    for (int i = 0; i < at.count; ++i) {
+        typename V::Raw r[2];
+        ring.take(i, r);
+        float xv[VEC], gv[VEC];
+        V::widen(r[0], xv);
+        V::widen(r[1], gv);
+        K.apply(P.act, xv, gv);
+        add_to(sa, gv);
+        fma_to(sb, gv, xv, sb);
     }
+    __syncthreads();   // the sums take the slots' place
+    float *gn_red = reinterpret_cast<float *>(gn_smem);
     const int nt = P.tx * P.ty, cb = P.tx * VEC, c0 = at.c - at.col * VEC;
     float *part = gn_red + 2 * nt * VEC, *csum = part + 2 * blockDim.x;
     channel_sums<VEC>(P, gn_red, part, csum, at.row < P.ty, sa, sb);
@@ -575,28 +576,24 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_sums_kernel(const __gr
 // instead.
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_apply_kernel(const __grid_constant__ GnParams P) {
-    extern __shared__ __align__(16) float gn_red[];
+    extern __shared__ __align__(16) uint8_t gn_smem[];
     using V = Pack<T, VEC>;
+    using Ring = GnRing<T, VEC, 2>;
     if (blockIdx.x < P.channel_blocks) {
-        join_channels(P, blockIdx.x, static_cast<int64_t>(P.N) * P.slabs, reinterpret_cast<double *>(gn_red));
+        join_channels(P, blockIdx.x, static_cast<int64_t>(P.N) * P.slabs, reinterpret_cast<double *>(gn_smem));
         return;
     }
     const GnPlace<VEC> at(P, gridDim.x - 1 - blockIdx.x);
     const int group0 = at.group(P, 0);
-    float *k1 = gn_red, *k2 = gn_red + P.gpc;
-    const T *x = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
-    const T *g = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c + at.p0 * P.g.sp;
+    float *k1 = reinterpret_cast<float *>(gn_smem + Ring::kSlotBytes), *k2 = k1 + P.gpc;
+    Ring ring(gn_smem, at.count);
+    ring.due[0] = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
+    ring.due[1] = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c + at.p0 * P.g.sp;
+    ring.step[0] = P.ty * P.x.sp;
+    ring.step[1] = P.ty * P.g.sp;
+    ring.begin();
     T *o = static_cast<T *>(P.out) + at.n * P.on + at.c + at.p0 * P.op;
-    const int64_t xstep = P.ty * P.x.sp, gstep = P.ty * P.g.sp, ostep = P.ty * P.op;
-    constexpr int U = 2;
-    typename V::Raw rx[U], rg[U];
-    if (at.count >= U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            rx[u] = V::load(x + u * xstep);
-            rg[u] = V::load(g + u * gstep);
-        }
-    }
+    const int64_t ostep = P.ty * P.op;
     GnSlope<VEC> K;
     K.template load<UNI>(P, at.n, group0, at.col * VEC, at.c, at.on);
     for (int j = threadIdx.x / 32; j < P.gpc; j += blockDim.x / 32) {
@@ -620,32 +617,18 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_apply_kernel(const __g
         c1[q] = -K.rstd[q] * k1[j];
         c2[q] = -K.rstd[q] * k2[j];
     });
-    auto one = [&](const typename V::Raw &rx, const typename V::Raw &rg, T *to) {
+#pragma unroll 2
+    for (int i = 0; i < at.count; ++i, o += ostep) {
+        typename V::Raw r[2];
+        ring.take(i, r);
         float xv[VEC], gv[VEC];
-        V::widen(rx, xv);
-        V::widen(rg, gv);
+        V::widen(r[0], xv);
+        V::widen(r[1], gv);
         K.apply(P.act, xv, gv);
         fma_to(xv, xv, c2, c1);
         fma_to(gv, gv, scale, xv);
-        V::store(to, gv);
-    };
-    int i = 0;
-    // (no second batch under way here: its registers would spill)
-    for (; i + U <= at.count; i += U) {
-        if (i > 0) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                rx[u] = V::load(x + u * xstep);
-                rg[u] = V::load(g + u * gstep);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) one(rx[u], rg[u], o + u * ostep);
-        x += U * xstep;
-        g += U * gstep;
-        o += U * ostep;
+        V::store(o, gv);
     }
-    if (i < at.count) one(V::load(x), V::load(g), o);
 }
 
 // ---------------------------------------------------------------- one pass
@@ -667,18 +650,6 @@ __device__ __forceinline__ void gn_cluster_arrive() {
 __device__ __forceinline__ void gn_cluster_wait() {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-template <int BYTES>
-__device__ __forceinline__ void gn_copy_async(uint32_t dst, const void *src) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void gn_copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 __device__ __forceinline__ uint32_t gn_cluster_id() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
