@@ -11,6 +11,12 @@
 
 namespace mqc {
 
+// Dependent launches: the second kernel of a call starts when the first one's
+// last blocks have, and sets up meanwhile; before it touches what the first
+// one leaves (or overwrites what it reads) it waits for that grid's end.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Values are widened exactly and rounded once, to nearest even.
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }

@@ -261,42 +261,36 @@ mqc_status launch(GnParams &P, const GnPlan &plan, const DeviceLimits &d, cudaSt
                 if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(group norm)");
                 allowed[d.device].store(true, std::memory_order_release);
             }
-            cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(static_cast<unsigned>(int64_t(P.N) * P.chunks * P.splits));
-            cfg.blockDim = dim3(P.threads);
-            cfg.dynamicSmemBytes = static_cast<size_t>(plan.smem);
-            cfg.stream = s;
-            cudaLaunchAttribute at[1];
-            at[0].id = cudaLaunchAttributeClusterDimension;
-            at[0].val.clusterDim.x = P.splits;
-            at[0].val.clusterDim.y = 1;
-            at[0].val.clusterDim.z = 1;
-            cfg.attrs = at;
-            cfg.numAttrs = 1;
-            cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P);
+            const Launch chip(int64_t(P.N) * P.chunks * P.splits, P.threads, P.splits, plan.smem, false, s);
+            cudaError_t e = cudaLaunchKernelEx(&chip.cfg, kernel, P);
             if (e != cudaSuccess) return cuda_fail(e, "group norm launch");
             if (channel_blocks > 0) {
-                gn_channels_kernel<<<channel_blocks, kGnThreads, 0, s>>>(P, P.N);
-                e = cudaGetLastError();
+                const Launch channels(channel_blocks, kGnThreads, 0, 0, true, s);
+                e = cudaLaunchKernelEx(&channels.cfg, gn_channels_kernel, P, int64_t(P.N));
                 if (e != cudaSuccess) return cuda_fail(e, "group norm launch");
             }
             return MQC_OK;
         }
     const unsigned grid = static_cast<unsigned>(int64_t(P.N) * P.slabs * P.chunks);
     const size_t nt = size_t(P.tx) * P.ty, groups = 2 * size_t(P.gpc) * 4;
+    cudaError_t e;
     if constexpr (BWD) {
         P.channel_blocks = channel_blocks;
         const size_t ring = GnRing<T, VEC, 2>::kSlotBytes;
         const size_t sums = 4 * (2 * nt * VEC + 2 * P.threads + 2 * size_t(P.tx) * VEC);
         const size_t join = P.threads / 32 * 2 * 32 * 8;
         gn_bwd_sums_kernel<T, VEC, UNI><<<grid, P.threads, std::max(ring, sums), s>>>(P);
-        gn_bwd_apply_kernel<T, VEC, UNI><<<grid + channel_blocks, P.threads, std::max(ring + groups, join), s>>>(P);
+        const Launch apply(int64_t(grid) + channel_blocks, P.threads, 0, std::max(ring + groups, join), true, s);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&apply.cfg, gn_bwd_apply_kernel<T, VEC, UNI>, P);
     } else {
         const size_t ring = GnRing<T, VEC, 1>::kSlotBytes;
-        gn_stats_kernel<T, VEC, UNI><<<grid, P.threads, std::max(ring, 4 * nt * (UNI ? 1 : P.seg) + groups), s>>>(P);
-        gn_apply_kernel<T, VEC, UNI><<<grid, P.threads, ring + groups, s>>>(P);
+        const size_t sums = 4 * nt * (UNI ? 1 : P.seg) + groups;
+        gn_stats_kernel<T, VEC, UNI><<<grid, P.threads, std::max(ring, sums), s>>>(P);
+        const Launch apply(grid, P.threads, 0, ring + groups, true, s);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = cudaLaunchKernelEx(&apply.cfg, gn_apply_kernel<T, VEC, UNI>, P);
     }
-    cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "group norm launch");
 }
 

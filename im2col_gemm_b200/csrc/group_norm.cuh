@@ -222,6 +222,7 @@ __device__ __forceinline__ void join_channels(const GnParams &P, int block, int6
 static __global__ void __launch_bounds__(kGnThreads) gn_channels_kernel(const __grid_constant__ GnParams P,
                                                                         int64_t rows) {
     __shared__ double sh[kGnThreads / 32 * 2 * 32];
+    wait_previous();
     join_channels(P, blockIdx.x, rows, sh);
 }
 
@@ -391,6 +392,7 @@ struct GnRing {
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_stats_kernel(const __grid_constant__ GnParams P) {
     extern __shared__ __align__(16) uint8_t gn_smem[];
+    let_next_start();
     using V = Pack<T, VEC>;
     const GnPlace<VEC> at(P, blockIdx.x);
     using Ring = GnRing<T, VEC, 1>;
@@ -469,6 +471,7 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_apply_kernel(const __grid_
         a[q] = P.gamma && at.on ? P.gamma[at.c + q] : 1.f;
         b[q] = P.beta && at.on ? P.beta[at.c + q] : 0.f;
     }
+    wait_previous();
     for (int g = threadIdx.x / 32; g < P.gpc; g += blockDim.x / 32) {
         const double total = static_cast<double>(P.HW) * P.D;
         double s = 0.0, dev = 0.0;
@@ -533,6 +536,7 @@ struct GnSlope {
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_sums_kernel(const __grid_constant__ GnParams P) {
     extern __shared__ __align__(16) uint8_t gn_smem[];
+    let_next_start();
     using V = Pack<T, VEC>;
     using Ring = GnRing<T, VEC, 2>;
     const GnPlace<VEC> at(P, blockIdx.x);
@@ -580,6 +584,7 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_apply_kernel(const __g
     using V = Pack<T, VEC>;
     using Ring = GnRing<T, VEC, 2>;
     if (blockIdx.x < P.channel_blocks) {
+        wait_previous();
         join_channels(P, blockIdx.x, static_cast<int64_t>(P.N) * P.slabs, reinterpret_cast<double *>(gn_smem));
         return;
     }
@@ -596,6 +601,7 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_apply_kernel(const __g
     const int64_t ostep = P.ty * P.op;
     GnSlope<VEC> K;
     K.template load<UNI>(P, at.n, group0, at.col * VEC, at.c, at.on);
+    wait_previous();
     for (int j = threadIdx.x / 32; j < P.gpc; j += blockDim.x / 32) {
         const double total = static_cast<double>(P.HW) * P.D;
         double s = 0.0, t = 0.0;
@@ -819,6 +825,7 @@ __global__ void __launch_bounds__(kGnThreads) gn_chip_fwd_kernel(const __grid_co
 // Backward.
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kGnThreads) gn_chip_bwd_kernel(const __grid_constant__ GnParams P) {
+    let_next_start();   // gn_channels_kernel
     extern __shared__ __align__(16) uint8_t gn_smem[];
     using V = Pack<T, VEC>;
     GnChip<T, VEC> K(P, gn_smem, true);

@@ -49,6 +49,32 @@ inline FastDiv make_fastdiv(int32_t d) {
     return f;
 }
 
+// The configuration of a launch in clusters; `after`: behind the call's previous
+// kernel, which it waits for by itself (wait_previous).
+struct Launch {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute at[2];
+    Launch(int64_t grid, int threads, int cluster, size_t smem, bool after, cudaStream_t stream) {
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cfg.attrs = at;
+        if (cluster > 0) {
+            at[0].id = cudaLaunchAttributeClusterDimension;
+            at[0].val.clusterDim.x = cluster;
+            at[0].val.clusterDim.y = 1;
+            at[0].val.clusterDim.z = 1;
+            cfg.numAttrs = 1;
+        }
+        if (after) {
+            at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+        }
+    }
+    Launch(const Launch &) = delete;
+};
+
 inline bool act_ok(int act) { return act >= MQC_ACT_NONE && act <= MQC_ACT_GELU; }
 inline int dtype_bytes(int dtype) { return dtype == MQC_F32 ? 4 : 2; }
 

@@ -91,25 +91,14 @@ mqc_status fill_params(LinParams &P, const Product &p, bool bf16, int rows, bool
 }
 
 mqc_status launch_group(const LinGroup &G, bool pair, bool bf16, int64_t grid, int cluster, int threads, int smem,
-                        const DeviceLimits &d, cudaStream_t stream) {
+                        bool after, const DeviceLimits &d, cudaStream_t stream) {
     if (grid > (int64_t(1) << 31) - 1) return fail(MQC_ERR_INVALID, "linear: too many tiles");
     void (*kernel)(LinGroup) = pair ? (bf16 ? linear_pair_kernel<__nv_bfloat16> : linear_pair_kernel<__half>)
                                     : (bf16 ? linear_tile_kernel<__nv_bfloat16> : linear_tile_kernel<__half>);
     mqc_status st = allow_smem(reinterpret_cast<const void *>(kernel), 2 * pair + bf16, d);
     if (st != MQC_OK) return st;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cluster;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, G);
+    const Launch launch(grid, threads, cluster, smem, after, stream);
+    cudaError_t e = cudaLaunchKernelEx(&launch.cfg, kernel, G);
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear kernel launch");
 }
 
@@ -187,8 +176,8 @@ PairPlan plan_pairs(const Product *const *p, int count, int pairs) {
 
 // One or two products on CTA pairs, the longer reduction's tiles first (they
 // are dealt out in turn, and the shorter ones even out the end).
-mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool bf16, const DeviceLimits &d,
-                        cudaStream_t stream) {
+mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool bf16, bool after,
+                        const DeviceLimits &d, cudaStream_t stream) {
     const int pairs = d.sms / 2;
     const Product *order[2] = {&p[0], count > 1 ? &p[1] : nullptr};
     if (count > 1 && p[1].kblocks() > p[0].kblocks()) std::swap(order[0], order[1]);
@@ -217,13 +206,13 @@ mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool 
     if (count > 1 && tiles >= pairs)
         deal(G.first, tiles - G.first, order[0]->kblocks(), order[1]->kblocks(), pairs, G.early, G.late_from);
     return launch_group(G, true, bf16, 2 * std::min<int64_t>(tiles, pairs), 2, kPairThreads,
-                        1024 + stages * stage + kPairStaging, d, stream);
+                        1024 + stages * stage + kPairStaging, after, d, stream);
 }
 
 // One or two products on single tiles.  A product's plan does not depend on
 // the other's presence, nor then do its bits.
-mqc_status launch_tiles(const Product *p, int count, const BiasGrad &bias, bool bf16, const DeviceLimits &d,
-                        cudaStream_t stream) {
+mqc_status launch_tiles(const Product *p, int count, const BiasGrad &bias, bool bf16, bool after,
+                        const DeviceLimits &d, cudaStream_t stream) {
     LinGroup G{};
     G.bias = bias;
     G.cluster = 1;
@@ -260,13 +249,15 @@ mqc_status launch_tiles(const Product *p, int count, const BiasGrad &bias, bool 
         if (st != MQC_OK) return st;
     }
     const int64_t extra = bias.gb ? round_up(ceil_div(bias.N, kLinThreads), G.cluster) : 0;
-    return launch_group(G, false, bf16, int64_t(G.tiles) * G.cluster + extra, G.cluster, kLinThreads, smem, d, stream);
+    return launch_group(G, false, bf16, int64_t(G.tiles) * G.cluster + extra, G.cluster, kLinThreads, smem, after, d,
+                        stream);
 }
 
 // The products of a call, and its bias gradient's last sums beside them: in
-// one launch when the same kernel suits them.
-mqc_status launch_products(const Product *p, int count, const BiasGrad &bias, int32_t dtype, const DeviceLimits &d,
-                           cudaStream_t stream) {
+// one launch when the same kernel suits them.  after: linear_prep_kernel runs
+// before them.
+mqc_status launch_products(const Product *p, int count, const BiasGrad &bias, int32_t dtype, bool after,
+                           const DeviceLimits &d, cudaStream_t stream) {
     const bool bf16 = dtype == MQC_BF16;
     bool pairs[2] = {};
     for (int i = 0; i < count; ++i) {
@@ -274,10 +265,11 @@ mqc_status launch_products(const Product *p, int count, const BiasGrad &bias, in
         pairs[i] = !one->swap() && plan_pairs(&one, 1, d.sms / 2).us < plan_tiles(*one, d.sms).us;
     }
     if (count > 1 && pairs[0] != pairs[1]) {
-        mqc_status st = launch_products(p, 1, bias, dtype, d, stream);
-        return st != MQC_OK ? st : launch_products(p + 1, 1, BiasGrad{}, dtype, d, stream);
+        mqc_status st = launch_products(p, 1, bias, dtype, after, d, stream);
+        return st != MQC_OK ? st : launch_products(p + 1, 1, BiasGrad{}, dtype, false, d, stream);
     }
-    return pairs[0] ? launch_pairs(p, count, bias, bf16, d, stream) : launch_tiles(p, count, bias, bf16, d, stream);
+    return pairs[0] ? launch_pairs(p, count, bias, bf16, after, d, stream)
+                    : launch_tiles(p, count, bias, bf16, after, d, stream);
 }
 
 // Bytes of a padded copy of a rows x cols matrix, and whether one is needed.
@@ -302,7 +294,7 @@ void plan_pack(PackJob &job, Operand &op, int64_t rows, int64_t cols, uint8_t *&
 }
 
 mqc_status launch_prep(const LinPrep &prep, int32_t dtype, cudaStream_t stream) {
-    const int64_t blocks = int64_t(prep.dz.blocks) + prep.pack[0].blocks + prep.pack[1].blocks;
+    const int64_t blocks = prep.blocks();
     if (blocks == 0) return MQC_OK;
     if (blocks > (int64_t(1) << 31) - 1) return fail(MQC_ERR_INVALID, "linear: too many blocks");
     const bool vec = prep.dz.ldg % 8 == 0 && (prep.dz.z == nullptr || prep.dz.ldz % 8 == 0);
@@ -434,7 +426,7 @@ mqc_status mqc_linear_fwd(const mqc_linear *l, const void *x, const void *w, con
     p.E.ldy = l->ldy;
     p.E.ldz = l->ldz;
     p.E.act = l->act;
-    return launch_products(&p, 1, BiasGrad{}, l->dtype, d, s);
+    return launch_products(&p, 1, BiasGrad{}, l->dtype, prep.blocks() > 0, d, s);
 }
 
 size_t mqc_linear_bwd_workspace_bytes(const mqc_linear *l) {
@@ -520,7 +512,7 @@ mqc_status mqc_linear_bwd(const mqc_linear *l, const void *g, const void *z, con
         p[count++].E.ldy = l->ldgw;
     }
     if ((st = launch_prep(prep, l->dtype, s)) != MQC_OK) return st;
-    if (count > 0) return launch_products(p, count, bias, l->dtype, d, s);
+    if (count > 0) return launch_products(p, count, bias, l->dtype, prep.blocks() > 0, d, s);
     linear_bias_grad_kernel<<<static_cast<unsigned>(ceil_div(l->N, 128)), 128, 0, s>>>(bias);
     cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MQC_OK : cuda_fail(e, "linear_bias_grad_kernel launch");

@@ -228,6 +228,7 @@ __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_c
     int id = blockIdx.x / G.cluster;
     const int place = blockIdx.x - id * G.cluster;
     if (id >= G.tiles) {   // clusters behind the tiles': the bias gradient
+        wait_previous();
         const int c = (blockIdx.x - G.tiles * G.cluster) * kLinThreads + threadIdx.x;
         if (c < G.bias.N) bias_grad_column(G.bias, c);
         return;
@@ -268,6 +269,8 @@ __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_c
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    wait_previous();
+    asm volatile("fence.proxy.async.global;" ::: "memory");   // the copies are read by TMA
     const uint32_t tmem = tmem_base;
     volatile int *abort = &abort_flag;
 
@@ -631,6 +634,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
     __syncthreads();
     cluster_sync();
     tc_fence_after();
+    wait_previous();
+    asm volatile("fence.proxy.async.global;" ::: "memory");   // the copies are read by TMA
     const uint32_t tmem = tmem_base;
 
     // tile t: bands of eight rows of tiles, column by column inside a band,
@@ -985,9 +990,11 @@ __device__ __forceinline__ void dz_block(const DzJob &J, int block) {
 struct LinPrep {
     DzJob dz;
     PackJob pack[2];
+    int64_t blocks() const { return int64_t(dz.blocks) + pack[0].blocks + pack[1].blocks; }
 };
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(256, 3) linear_prep_kernel(const __grid_constant__ LinPrep P) {
+    let_next_start();
     int b = blockIdx.x;
     if (b < P.dz.blocks) return dz_block<T, VEC>(P.dz, b);
     b -= P.dz.blocks;
