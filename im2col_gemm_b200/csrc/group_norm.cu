@@ -215,13 +215,18 @@ struct GnPlan {
 GnPlan make_plan(GnParams &P, int vec, int32_t dtype, bool bwd) {
     GnPlan p{vec, false, 0, 0, 0};
     p.chip = plan_chip(P, vec, dtype, bwd, p.smem);
-    // Clusters of 16 CTAs with nearly all of their shared memory leave an SM
-    // nothing to overlap their phases with; once the tensors are large, two
-    // passes of many small blocks are faster, the second one partly out of L2:
-    // 16x64x160x160 bf16 39.8 against 44.1 us, backward 70.7 against 114; at
-    // 26 MB (4x64x160x160) 21.6 against 17.3.
+    // On chip a tensor is read once, but a CTA's phases overlap with nobody's
+    // when it takes most of an SM, and clusters of many CTAs fill the chip in
+    // fewer, longer rounds; two passes of small blocks overlap better, and the
+    // second one finds what the first read last in L2.  From 118 shapes of 4 to
+    // 380 MB, the slower form within 16% wherever this rule picks it; e.g. bf16
+    // forward, on chip against two passes: 24x512x20x20 (one CTA) 8.3, 12.0 us;
+    // 8x128x80x80 (four) 11.3, 16.3; 24x128x80x80 27.9, 27.2; 8x64x160x160
+    // (16) 27.8, 19.7; backward 24x512x20x20 15.1, 17.7; 24x256x40x40 (two)
+    // 35.5, 24.5; 8x128x80x80 (16) 28.0, 20.1.
     const int64_t bytes = int64_t(P.N) * P.C * P.HW * dtype_bytes(dtype) * (bwd ? 3 : 2);
-    if (P.splits == 16 && bytes > (int64_t(32) << 20)) p.chip = false;
+    if (bwd ? P.splits > 4 || bytes > (int64_t(32) << 20) : P.splits > 2 && bytes * P.splits > 200000000)
+        p.chip = false;
     if (p.chip) {
         P.slabs = 1;
         P.pieces = 1;
@@ -280,14 +285,14 @@ mqc_status launch(GnParams &P, const GnPlan &plan, const DeviceLimits &d, cudaSt
         const size_t sums = 4 * (2 * nt * VEC + 2 * P.threads + 2 * size_t(P.tx) * VEC);
         const size_t join = P.threads / 32 * 2 * 32 * 8;
         gn_bwd_sums_kernel<T, VEC, UNI><<<grid, P.threads, std::max(ring, sums), s>>>(P);
-        const Launch apply(int64_t(grid) + channel_blocks, P.threads, 0, std::max(ring + groups, join), true, s);
+        const Launch apply(int64_t(grid) + channel_blocks, P.threads, 0, std::max(ring + kJoinBytes + groups, join), true, s);
         e = cudaGetLastError();
         if (e == cudaSuccess) e = cudaLaunchKernelEx(&apply.cfg, gn_bwd_apply_kernel<T, VEC, UNI>, P);
     } else {
         const size_t ring = GnRing<T, VEC, 1>::kSlotBytes;
         const size_t sums = 4 * nt * (UNI ? 1 : P.seg) + groups;
         gn_stats_kernel<T, VEC, UNI><<<grid, P.threads, std::max(ring, sums), s>>>(P);
-        const Launch apply(grid, P.threads, 0, ring + groups, true, s);
+        const Launch apply(grid, P.threads, 0, ring + kJoinBytes + groups, true, s);
         e = cudaGetLastError();
         if (e == cudaSuccess) e = cudaLaunchKernelEx(&apply.cfg, gn_apply_kernel<T, VEC, UNI>, P);
     }

@@ -166,7 +166,7 @@ struct GnRunning {
     }
     __device__ __forceinline__ void start(const float (&v)[VEC]) {
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) first[q] = -v[q];
+        for (int q = 0; q < VEC; ++q) first[q] = isfinite(v[q]) ? -v[q] : 0.f;   // an infinite mean stays infinite
     }
     __device__ __forceinline__ void add(float (&v)[VEC]) {
         add_to(v, first);
@@ -186,7 +186,7 @@ struct GnRunning {
 };
 
 // Channels' sums joined over `rows` partial rows ([row][2][C]), 32 channels a
-// block, a warp every (blockDim / 32)-th row with four loads in flight; the
+// block, a warp every (blockDim / 32)-th row with eight loads in flight; the
 // warps' shares in warp order.  sh: [warps][2][32] doubles.
 __device__ __forceinline__ void join_channels(const GnParams &P, int block, int64_t rows, double *sh) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
@@ -194,16 +194,16 @@ __device__ __forceinline__ void join_channels(const GnParams &P, int block, int6
     double a = 0.0, b = 0.0;
     if (c < P.C) {
         const float *at = P.part + c;
-        for (int64_t e = warp; e < rows; e += 4 * warps) {
-            float va[4], vb[4];
+        for (int64_t e = warp; e < rows; e += 8 * warps) {
+            float va[8], vb[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 8; ++u) {
                 const int64_t r = e + u * warps;
                 va[u] = r < rows ? at[r * 2 * P.C] : 0.f;
                 vb[u] = r < rows ? at[(r * 2 + 1) * P.C] : 0.f;
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 8; ++u) {
                 a += va[u];
                 b += vb[u];
             }
@@ -339,7 +339,7 @@ __device__ __forceinline__ void gn_copy_wait() {
 // land in its own slots of shared memory ([slot][tensor][thread]), so the depth
 // costs no registers and the order needs no barrier.  (Batches loaded ahead
 // into registers: 16x64x160x160 bf16 forward took 38.9 us, now 34.7, and
-// 16x128x80x80 fp32 backward 100.6, now 88.7.)  Elements of two
+// 32x128x80x80 fp32 backward 100.6, now 88.7.)  Elements of two
 // bytes, too small for asynchronous copies, are loaded when they are due.
 template <typename T, int VEC, int NT>
 struct GnRing {
@@ -435,18 +435,63 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// The partial sums of group g of the block's chunk, over all slabs and pieces:
-// f(the pair, the values it covers), a lane every 32nd.
-template <int VEC, typename F>
-__device__ __forceinline__ void each_part(const GnParams &P, const GnPlace<VEC> &at, int g, F &&f) {
+// Sums over the partial results (pairs) of each group of the block's chunk, all
+// slabs and pieces: f(first pair, pair, the values it covers, sums) adds one to
+// a pair of sums, out(group, first pair, sums) gets the total.  Neighbouring
+// threads read neighbouring groups, and each has four loads under way: with two
+// images the pairs of some 200 slabs are read by every block (a warp a group,
+// one load after another, 2x128x80x80 fp32 took 20.6 us, now 11.8).
+constexpr int kJoinBytes = kPassThreads * sizeof(double2);
+template <int VEC, typename F, typename O>
+__device__ __forceinline__ void join_parts(const GnParams &P, const GnPlace<VEC> &at, double2 *sh, F &&f, O &&out) {
     const float2 *part = reinterpret_cast<const float2 *>(P.gpart) + static_cast<int64_t>(at.n) * P.slabs * P.chunks * P.gpc;
-    const int first = P.pieces > 1 ? at.chunk - at.chunk % P.pieces : at.chunk;
-    for (int e = threadIdx.x % 32; e < P.slabs * P.pieces; e += 32) {
-        const int s = P.pieces > 1 ? e / P.pieces : e, k = e - s * P.pieces;
-        const int channels = P.pieces > 1 ? min(P.width, P.D - k * P.width) : P.D;
-        f(part[(static_cast<int64_t>(s) * P.chunks + first + k) * P.gpc + g],
-          static_cast<float>(min(P.HW - s * P.slab, P.slab)) * channels);
+    const int first = P.pieces > 1 ? at.chunk - at.chunk % P.pieces : at.chunk, rows = P.slabs * P.pieces;
+    const int per = kPassThreads / P.gpc;   // a chunk of whole groups has 256 of them at most
+    const int r = threadIdx.x / P.gpc, g = threadIdx.x - r * P.gpc;
+    const float2 *from = part + static_cast<int64_t>(first) * P.gpc;
+    if (r < per) {
+        const float2 head = from[g];
+        double2 sum = make_double2(0.0, 0.0);
+        for (int e0 = r; e0 < rows; e0 += 4 * per) {
+            float2 v[4];
+            float n[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int e = e0 + u * per;
+                const int s = P.pieces > 1 ? e / P.pieces : e, k = e - s * P.pieces;
+                const int channels = P.pieces > 1 ? min(P.width, P.D - k * P.width) : P.D;
+                n[u] = static_cast<float>(min(P.HW - s * P.slab, P.slab)) * channels;
+                if (e < rows) v[u] = from[(static_cast<int64_t>(s) * P.chunks + k) * P.gpc + g];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (e0 + u * per < rows) f(head, v[u], n[u], sum);
+        }
+        sh[threadIdx.x] = sum;
     }
+    __syncthreads();
+    if (per <= 16) {
+        if (r == 0) {
+            double2 sum = sh[g];
+            for (int k = 1; k < per; ++k) {
+                sum.x += sh[k * P.gpc + g].x;
+                sum.y += sh[k * P.gpc + g].y;
+            }
+            out(g, from[g], sum);
+        }
+    } else {
+        for (int j = threadIdx.x / 32; j < P.gpc; j += kPassThreads / 32) {
+            double2 sum = make_double2(0.0, 0.0);
+            for (int k = threadIdx.x % 32; k < per; k += 32) {
+                sum.x += sh[k * P.gpc + j].x;
+                sum.y += sh[k * P.gpc + j].y;
+            }
+            sum.x = warp_sum(sum.x);
+            sum.y = warp_sum(sum.y);
+            if (threadIdx.x % 32 == 0) out(j, from[j], sum);
+        }
+    }
+    __syncthreads();
 }
 
 // Second pass: y = act((x - mean) (rstd gamma) + beta).  Blocks go from the
@@ -458,7 +503,7 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_apply_kernel(const __grid_
     using V = Pack<T, VEC>;
     using Ring = GnRing<T, VEC, 1>;
     const GnPlace<VEC> at(P, gridDim.x - 1 - blockIdx.x);
-    float *mean = reinterpret_cast<float *>(gn_smem + Ring::kSlotBytes), *rstd = mean + P.gpc;
+    float *mean = reinterpret_cast<float *>(gn_smem + Ring::kSlotBytes + kJoinBytes), *rstd = mean + P.gpc;
     Ring ring(gn_smem, at.count);
     ring.due[0] = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
     ring.step[0] = P.ty * P.x.sp;
@@ -472,24 +517,25 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_apply_kernel(const __grid_
         b[q] = P.beta && at.on ? P.beta[at.c + q] : 0.f;
     }
     wait_previous();
-    for (int g = threadIdx.x / 32; g < P.gpc; g += blockDim.x / 32) {
-        const double total = static_cast<double>(P.HW) * P.D;
-        double s = 0.0, dev = 0.0;
-        each_part(P, at, g, [&](float2 v, float n) { s += static_cast<double>(n) * v.x; });
-        const double mu = warp_sum(s) / total;
-        each_part(P, at, g, [&](float2 v, float n) { dev += v.y + n * (v.x - mu) * (v.x - mu); });
-        dev = warp_sum(dev) / total;
-        if (threadIdx.x % 32 == 0) {
-            mean[g] = static_cast<float>(mu);
-            rstd[g] = static_cast<float>(1.0 / sqrt(dev + P.eps));
-            if (at.slab == 0 && (P.pieces == 1 || at.chunk % P.pieces == 0)) {
-                const int64_t i = static_cast<int64_t>(at.n) * P.G + at.group(P, g);
-                P.mean[i] = mean[g];
-                P.rstd[i] = rstd[g];
-            }
-        }
-    }
-    __syncthreads();
+    // Means about the first slab's (0 if that is not finite), in 64 bits: what
+    // cancels in the deviations is the spread of the slabs' means alone.
+    const double total = static_cast<double>(P.HW) * P.D;
+    join_parts(P, at, reinterpret_cast<double2 *>(gn_smem + Ring::kSlotBytes),
+               [](float2 head, float2 v, float n, double2 &sum) {
+                   const double d = static_cast<double>(v.x) - (isfinite(head.x) ? head.x : 0.f);
+                   sum.x += n * d;
+                   sum.y += v.y + n * d * d;
+               },
+               [&](int g, float2 head, double2 sum) {
+                   const double d = sum.x / total, var = fmax(sum.y / total - d * d, 0.0);
+                   mean[g] = static_cast<float>((isfinite(head.x) ? head.x : 0.f) + d);
+                   rstd[g] = static_cast<float>(1.0 / sqrt((isfinite(d) ? var : d - d) + P.eps));
+                   if (at.slab == 0 && (P.pieces == 1 || at.chunk % P.pieces == 0)) {
+                       const int64_t i = static_cast<int64_t>(at.n) * P.G + at.group(P, g);
+                       P.mean[i] = mean[g];
+                       P.rstd[i] = rstd[g];
+                   }
+               });
     per_channel_group<VEC, UNI>(at.col * VEC, P.D, [&](int q, int g) {
         m[q] = -mean[g];
         a[q] *= rstd[g];
@@ -590,7 +636,7 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_apply_kernel(const __g
     }
     const GnPlace<VEC> at(P, gridDim.x - 1 - blockIdx.x);
     const int group0 = at.group(P, 0);
-    float *k1 = reinterpret_cast<float *>(gn_smem + Ring::kSlotBytes), *k2 = k1 + P.gpc;
+    float *k1 = reinterpret_cast<float *>(gn_smem + Ring::kSlotBytes + kJoinBytes), *k2 = k1 + P.gpc;
     Ring ring(gn_smem, at.count);
     ring.due[0] = static_cast<const T *>(P.x.p) + at.n * P.x.sn + at.c + at.p0 * P.x.sp;
     ring.due[1] = static_cast<const T *>(P.g.p) + at.n * P.g.sn + at.c + at.p0 * P.g.sp;
@@ -602,21 +648,16 @@ __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_apply_kernel(const __g
     GnSlope<VEC> K;
     K.template load<UNI>(P, at.n, group0, at.col * VEC, at.c, at.on);
     wait_previous();
-    for (int j = threadIdx.x / 32; j < P.gpc; j += blockDim.x / 32) {
-        const double total = static_cast<double>(P.HW) * P.D;
-        double s = 0.0, t = 0.0;
-        each_part(P, at, j, [&](float2 v, float) {
-            s += v.x;
-            t += v.y;
-        });
-        s = warp_sum(s);
-        t = warp_sum(t);
-        if (threadIdx.x % 32 == 0) {
-            k1[j] = static_cast<float>(s / total);
-            k2[j] = static_cast<float>(t / total);
-        }
-    }
-    __syncthreads();
+    const double total = static_cast<double>(P.HW) * P.D;
+    join_parts(P, at, reinterpret_cast<double2 *>(gn_smem + Ring::kSlotBytes),
+               [](float2, float2 v, float, double2 &sum) {
+                   sum.x += v.x;
+                   sum.y += v.y;
+               },
+               [&](int j, float2, double2 sum) {
+                   k1[j] = static_cast<float>(sum.x / total);
+                   k2[j] = static_cast<float>(sum.y / total);
+               });
     float scale[VEC], c1[VEC], c2[VEC];
     per_channel_group<VEC, UNI>(at.col * VEC, P.D, [&](int q, int j) {
         scale[q] = K.rstd[q] * K.gamma[q];

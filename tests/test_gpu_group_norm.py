@@ -296,3 +296,43 @@ def test_helper_refusals(mqc):
                  lambda: mqc.group_norm_fwd(t["x"], 4, out=t["x"][:1])):
         with pytest.raises(ValueError):
             call()
+
+
+# Large images, whose statistics are joined from the sums of many slabs: 256
+# groups of one channel side by side, one group, groups of two, eight channels.
+SLABS = [(1, 256, 180, 180, 256), (1, 64, 300, 300, 1), (2, 512, 60, 60, 256), (1, 8, 250, 250, 8)]
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("shape", SLABS)
+def test_statistics_of_many_slabs(mqc, shape, dtype):
+    *dims, groups = shape
+    t = make(*dims, dtype, seed=groups)
+    check_fwd(mqc, t, groups, 2)
+    check_bwd(mqc, t, groups, 2)
+
+
+@pytest.mark.parametrize("shape", SLABS)
+def test_offsets_of_many_slabs(mqc, shape):
+    """A mean of 1000 that drifts by 8 over the image: slabs with means of
+    their own, whose spread belongs to the variance."""
+    *dims, groups = shape
+    t = make(*dims, F32, offset=0.0)
+    drift = torch.linspace(996.0, 1004.0, dims[2], device="cuda").view(1, 1, -1, 1)
+    t["x"] = (t["x"] + drift).contiguous(memory_format=torch.channels_last)
+    check_fwd(mqc, t, groups, 0)
+
+
+@pytest.mark.parametrize("where", [(0, 0), (90, 17)])
+def test_infinity_in_a_slab(mqc, where):
+    """One infinity, in the first slab or a later one: its group's mean is
+    infinite, its outputs NaN, and the other groups keep their bits."""
+    t = make(1, 64, 180, 180, F32)
+    clean = mqc.group_norm_fwd(t["x"], 32, t["gamma"], t["beta"], EPS, 2)
+    x = t["x"].clone(memory_format=torch.channels_last)
+    x[0, 4, where[0], where[1]] = float("inf")
+    y, mean, rstd = mqc.group_norm_fwd(x, 32, t["gamma"], t["beta"], EPS, 2)
+    others = [g for g in range(32) if g != 2]
+    assert mean[0, 2] == float("inf") and torch.isnan(rstd[0, 2]) and torch.isnan(y[0, 4:6]).all()
+    assert torch.equal(mean[0, others], clean[1][0, others]) and torch.equal(rstd[0, others], clean[2][0, others])
+    assert torch.equal(y[0, 6:], clean[0][0, 6:]) and torch.equal(y[0, :4], clean[0][0, :4])
