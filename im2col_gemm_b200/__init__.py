@@ -582,7 +582,8 @@ def group_norm_fwd(x, groups: int, gamma=None, beta=None, eps: float = 1e-5, act
     _params(x, shape[1], gamma, beta)
     xd = _image_desc(x, shape)
     y, yd = _image_like(x, xd, out)
-    mean, rstd = x.new_empty((2, shape[0], max(groups, 0)), dtype=_torch().float32).unbind(0)
+    mean = x.new_empty((shape[0], max(groups, 0)), dtype=_torch().float32)
+    rstd = _torch().empty_like(mean)
     ws, at, nws = _scratch(lib.mqc_group_norm_fwd_workspace_bytes(xd, yd, dt, groups), x, workspace)
     check(lib.mqc_group_norm_fwd(x.data_ptr(), xd, dt, _address(gamma), _address(beta), groups, eps, act, y.data_ptr(),
                                  yd, mean.data_ptr(), rstd.data_ptr(), at, nws, _CUDA["stream"](x.get_device())))
@@ -601,7 +602,8 @@ def group_norm_bwd(g, x, groups: int, mean, rstd, gamma=None, beta=None, act: in
     _params(x, shape[0] * groups, mean, rstd)
     gd, xd = _image_desc(g, shape), _image_desc(x, shape)
     gx, gxd = _image_like(x, xd, out)
-    ggamma, gbeta = x.new_empty((2, shape[1]), dtype=_torch().float32).unbind(0)
+    ggamma = x.new_empty(shape[1], dtype=_torch().float32)
+    gbeta = _torch().empty_like(ggamma)
     ws, at, nws = _scratch(lib.mqc_group_norm_bwd_workspace_bytes(gd, xd, gxd, dt, groups), x, workspace)
     check(lib.mqc_group_norm_bwd(g.data_ptr(), gd, x.data_ptr(), xd, dt, _address(gamma), _address(beta),
                                  mean.data_ptr(), rstd.data_ptr(), groups, act, gx.data_ptr(), gxd, ggamma.data_ptr(),

@@ -216,6 +216,10 @@ __device__ __forceinline__ void tile_epilogue(const LinParams &P, const float *p
 // of distributed shared memory), and after another barrier every CTA sums what
 // it got in rank order and stores it.  So a product with few tiles uses all
 // SMs in one launch, without a workspace, and gives the same bits each time.
+// Small products are bound by latency: a launch, the first stages, a barrier
+// for the join, the epilogue.  128 x 1003 x 515 fp16 takes 10.7 us with the
+// copies of both operands before it, where its 1.4 MB would take 0.2; both
+// gradients of 509 x 777 x 1003 19 us with the copies and dz.
 template <typename T>
 __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_constant__ LinGroup G) {
     extern __shared__ uint8_t lin_smem_raw[];
@@ -593,6 +597,11 @@ __device__ __forceinline__ int pair_tile(const LinGroup &G, int c, int pairs, in
 // accumulators of 128 x bn, so that the epilogue of one tile runs beside the
 // products of the next.  All full-stage signals go to the first CTA, which
 // issues the products for both.
+// Bound by the tensor cores: 8192 x 4096 x 4096 bf16 with bias, GELU, residual
+// and z stored takes 205 us, 1340 TFLOP/s (78% of a library product's rate in
+// a burst, 92% of its rate under the power limit), the tensor pipe active for
+// 83% of it; both gradients of 8192 x 2048 x 2048 with dz and the bias' sums
+// before them 117 us.  (Tiles of lone CTAs: 306 and 170 us.)
 template <typename T>
 __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __grid_constant__ LinGroup G) {
     extern __shared__ uint8_t lin_smem_raw[];
@@ -792,8 +801,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
 // A block of eight warps computes RN features; the warps share the reduction
 // in chunks of 256 steps, a lane 8 of them from 16-byte loads (VEC), and are
 // joined in warp order.  Nothing but the loads' latency stands between the
-// launch and the last byte; the tensor-core form spends as long again on
-// filling its pipeline and joining its CTAs (14.1 us at 1 x 4096 x 4096).
+// launch and the last byte: 1 x 4096 x 4096 takes 8.8 us, 3.8 TB/s (a plain
+// copy of 6.45 TB/s would read the weights in 5.2); the tensor-core form spends
+// more on filling its pipeline and joining its CTAs (11.4 us).
 template <typename T, int MT, int RN, bool VEC>
 __global__ void __launch_bounds__(256) linear_few_kernel(const LinFew P) {
     __shared__ float sums[8][RN * MT];
@@ -900,7 +910,8 @@ __device__ __forceinline__ void pack_rows(const PackJob &J, int block) {
 
 // dz = g * act'(z) (rounded to the operand type of the products) and the
 // column sums of the unrounded dz over a slab of rows.  A block is 32 lanes x
-// 8 row groups; a lane owns 8 columns.  VEC: whole 16-byte loads.
+// 8 row groups; a lane owns 8 columns.  VEC: whole 16-byte loads.  Bound by
+// memory: 8192 x 2048 bf16 with z (100 MB) takes 17 us, 5.9 TB/s.
 constexpr int kDzRows = 8;
 struct DzJob {
     const void *g, *z;               // z NULL: dz = g

@@ -170,29 +170,10 @@ uint32_t map_key_hash(const MapKey &k) {
 // Encode a tiled map over 1-byte codes.  dims[0] is contiguous; strides are
 // the byte strides of dims[1..rank-1]; the inner box is 32*wkb bytes with the
 // matching shared-memory swizzle.
-mqc_status encode_codes_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
-                            const uint64_t *strides, const uint32_t *box, int wkb) {
+mqc_status encode_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims, const uint64_t *strides,
+                      const uint32_t *box, int wkb) {
     mqc_status st = get_encoder();
     if (st != MQC_OK) return st;
-    MapKey key;
-    memset(&key, 0, sizeof key);
-    key.base = reinterpret_cast<uint64_t>(base);
-    key.rank = rank;
-    key.wkb = wkb;
-    for (int i = 0; i < rank && i < 5; ++i) {
-        key.dims[i] = dims[i];
-        key.box[i] = box[i];
-    }
-    for (int i = 0; i + 1 < rank && i < 4; ++i) key.strides[i] = strides[i];
-    const uint32_t slot = map_key_hash(key) % kMapCacheSlots;
-    {
-        std::lock_guard<std::mutex> lock(g_map_mutex);
-        const MapSlot &c = g_map_cache[slot];
-        if (c.used && memcmp(&c.key, &key, sizeof key) == 0) {
-            *map = c.map;
-            return MQC_OK;
-        }
-    }
     cuuint64_t gd[5], gs[4];
     cuuint32_t bx[5], es[5];
     for (int i = 0; i < rank; ++i) {
@@ -215,15 +196,40 @@ mqc_status encode_codes_map(CUtensorMap *map, const void *base, int rank, const 
     CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void *>(base), gd, gs, bx, es,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(MQC_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
-    if (rank <= 5) {
+    return r == CUDA_SUCCESS ? MQC_OK : fail(MQC_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+}
+
+// The same through the cache.
+mqc_status encode_codes_map(CUtensorMap *map, const void *base, int rank, const uint64_t *dims,
+                            const uint64_t *strides, const uint32_t *box, int wkb) {
+    MapKey key;
+    memset(&key, 0, sizeof key);
+    key.base = reinterpret_cast<uint64_t>(base);
+    key.rank = rank;
+    key.wkb = wkb;
+    for (int i = 0; i < rank && i < 5; ++i) {
+        key.dims[i] = dims[i];
+        key.box[i] = box[i];
+    }
+    for (int i = 0; i + 1 < rank && i < 4; ++i) key.strides[i] = strides[i];
+    const uint32_t slot = map_key_hash(key) % kMapCacheSlots;
+    {
+        std::lock_guard<std::mutex> lock(g_map_mutex);
+        const MapSlot &c = g_map_cache[slot];
+        if (c.used && memcmp(&c.key, &key, sizeof key) == 0) {
+            *map = c.map;
+            return MQC_OK;
+        }
+    }
+    mqc_status st = encode_map(map, base, rank, dims, strides, box, wkb);
+    if (st == MQC_OK && rank <= 5) {
         std::lock_guard<std::mutex> lock(g_map_mutex);
         MapSlot &c = g_map_cache[slot];
         memcpy(&c.key, &key, sizeof key);
         c.map = *map;
         c.used = true;
     }
-    return MQC_OK;
+    return st;
 }
 
 }  // namespace
@@ -245,7 +251,7 @@ mqc_status encode_matrix_map(CUtensorMap *map, const void *base, int64_t rows, i
     const uint64_t dims[2] = {static_cast<uint64_t>(cols) * 2, static_cast<uint64_t>(rows)};
     const uint64_t strides[1] = {static_cast<uint64_t>(ld) * 2};
     const uint32_t box[2] = {static_cast<uint32_t>(box_bytes), static_cast<uint32_t>(box_rows)};
-    return encode_codes_map(map, base, 2, dims, strides, box, box_bytes / 32);
+    return encode_map(map, base, 2, dims, strides, box, box_bytes / 32);
 }
 
 }  // namespace mqc
