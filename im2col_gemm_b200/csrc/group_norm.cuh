@@ -388,7 +388,12 @@ struct GnRing {
     }
 };
 
-// First pass: mean and squared deviations of each group (or piece) of the slab.
+// First pass: mean and squared deviations of each group (or piece) of the slab,
+// about the thread's first value, joined by means and squared deviations (Chan
+// et al.): no large squares are subtracted.  Both forward passes together read
+// 16x64x160x160 bf16 twice and write it once (157 MB) in 32.1 us, 4.9 TB/s;
+// read once it would take 16.3, but no image's group fits an SM, and clusters
+// that share one took 44.
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_stats_kernel(const __grid_constant__ GnParams P) {
     extern __shared__ __align__(16) uint8_t gn_smem[];
@@ -579,6 +584,9 @@ struct GnSlope {
 };
 
 // First pass: sums of dz and dz xhat, by channel and (times gamma) by group.
+// dz is computed again by the second pass: both passes read x and g (and SiLU's
+// exponential, twice, keeps the issue slots half busy).  32x128x80x80 fp32:
+// 524 MB in 84 us, 6.2 TB/s; 128x256x14x14 bf16 (64 MB) 19 us.
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_sums_kernel(const __grid_constant__ GnParams P) {
     extern __shared__ __align__(16) uint8_t gn_smem[];
@@ -709,7 +717,9 @@ __device__ __forceinline__ uint32_t gn_cluster_id() {
 // shared memory, all copies in flight at once, and reads them again for the
 // second pass; so only the sums meet barriers.  Sums go over the CTA in shared
 // memory and over the cluster through distributed shared memory, always in the
-// same order.
+// same order.  Bound by latency (the copies, two barriers, the stores, one
+// after another) unless several CTAs share an SM: 1x256x14x14 bf16 4.4 us;
+// 7x320x45x37 fp32 (30 MB, 112 CTAs of 147 KB, not quite one an SM) 11.9.
 template <typename T, int VEC>
 struct GnChip {
     static constexpr int kBytes = VEC * sizeof(T);
