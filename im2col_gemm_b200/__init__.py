@@ -498,9 +498,13 @@ def _on_device(fn):
     """Runs fn with its first tensor's device current, so that the launches are
     that device's, and on its current stream (the last argument)."""
     import functools
+    first = fn.__code__.co_varnames[0]
 
     @functools.wraps(fn)
-    def call(t, *args, **kwargs):
+    def call(*args, **kwargs):
+        t = args[0] if args else kwargs.get(first)
+        if t is None:
+            raise TypeError(f"{fn.__name__}() needs {first}")
         if not t.is_cuda:
             raise ValueError("the tensors must be on a CUDA device")
         if not _DTYPES:
@@ -508,8 +512,8 @@ def _on_device(fn):
         device = t.get_device()
         if _CUDA["count"] > 1 and device != _torch().cuda.current_device():
             with _torch().cuda.device(device):
-                return fn(t, *args, **kwargs)
-        return fn(t, *args, **kwargs)
+                return fn(*args, **kwargs)
+        return fn(*args, **kwargs)
 
     return call
 
@@ -549,6 +553,8 @@ def _scratch(nbytes: int, like, workspace):
             return None, None, 0
         workspace = like.new_empty(nbytes, dtype=_torch().uint8)
         return workspace, workspace.data_ptr(), nbytes
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"expected a contiguous workspace on {like.device}, got one on {workspace.device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

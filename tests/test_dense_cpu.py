@@ -189,3 +189,28 @@ def test_helpers_refuse_host_tensors_and_wrong_types(mqc):
                  lambda: mqc.group_norm_fwd(x.view(1, 4, 2, 4), 2)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_helpers_take_their_first_tensor_by_name(mqc):
+    x = torch.zeros(4, 8, dtype=torch.bfloat16)
+    for call in (lambda: mqc.linear_fwd(x=x, w=x), lambda: mqc.dropout_fwd(x=x, p=0.5, seed=1),
+                 lambda: mqc.dropout_bwd(p=0.5, seed=1, g=x)):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    with pytest.raises(TypeError):
+        mqc.linear_fwd(w=x)
+
+
+def test_workspace_of_another_device_or_with_gaps_is_refused(mqc):
+    class OnDevice:   # what the check looks at
+        device = "cuda:0"
+
+        def get_device(self):
+            return 0
+
+    with pytest.raises(ValueError, match="workspace"):
+        mqc._scratch(64, OnDevice(), torch.empty(64, dtype=torch.uint8))
+    host = torch.empty(128, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace"):
+        mqc._scratch(64, host, host[::2])
+    assert mqc._scratch(64, host, host)[2] == 128
