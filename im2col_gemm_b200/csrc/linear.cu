@@ -211,6 +211,10 @@ mqc_status launch_pairs(const Product *p, int count, const BiasGrad &bias, bool 
 
 // One or two products on single tiles.  A product's plan does not depend on
 // the other's presence, nor then do its bits.
+// The room for a CTA's part of a tile also keeps the CTAs that fit on an SM to
+// its 512 columns of tensor memory together (at worst eight with 64 for 48
+// tokens, in 25.6 KB each), so that no cluster waits for
+// columns which another, waiting one holds.
 mqc_status launch_tiles(const Product *p, int count, const BiasGrad &bias, bool bf16, bool after,
                         const DeviceLimits &d, cudaStream_t stream) {
     LinGroup G{};
