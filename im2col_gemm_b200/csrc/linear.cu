@@ -316,14 +316,19 @@ mqc_status launch_prep(const LinPrep &prep, int32_t dtype, cudaStream_t stream) 
 
 // One to eight tokens (linear_few_kernel).  Four features a block where that
 // still leaves several blocks an SM, else one.
-// One or two tokens always; up to four (eight, if the tensor-core form would
-// have to copy operands first) where the weights are few: at 4096 x 4096 it
-// takes 8.4 us with one token, 11.0 with two and 14.6 with three, the tensor
-// cores 11.4 with any up to 16; at 1024 x 1024 2.7, 3.0 and 4.5 against 6.1.
+// One token always, a few where the weights are few; at N x K this form against
+// the tensor cores', in us:
+//   tokens        1            2            4            6            8
+//   1024 x 1024    2.7,  6.2    2.9,  6.3    5.2,  6.3    6.0,  6.3    6.7,  6.5
+//   2048 x 2048    3.4,  7.8    5.1,  7.9    6.1,  7.9    7.2,  7.9    8.0,  7.9
+//   4096 x 4096    8.6, 11.9   11.5, 11.8   17.1, 12.1   20.2, 12.1
+//   8192 x 8192   25.7, 29.2   30.9, 28.6   47.5, 28.7
+// (where those would have to copy operands first, two and eight).
 bool few_tokens(const mqc_linear *l) {
-    if (l->M <= 2) return true;
-    if (int64_t(l->N) * l->K > int64_t(1) << 22) return false;
-    return l->M <= 4 || (l->M <= 8 && (needs_pack(l->ldx) || needs_pack(l->ldw)));
+    const bool copies = needs_pack(l->ldx) || needs_pack(l->ldw);
+    const int64_t weights = int64_t(l->N) * l->K;
+    if (l->M <= 2) return l->M == 1 || copies || weights <= int64_t(1) << 24;
+    return weights <= int64_t(1) << 22 && l->M <= (copies ? 8 : 6);
 }
 template <typename T, int MT, int RN>
 void launch_few_as(const LinFew &P, bool vec, cudaStream_t s) {
