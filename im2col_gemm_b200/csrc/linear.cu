@@ -106,7 +106,8 @@ mqc_status launch_group(const LinGroup &G, bool pair, bool bf16, int64_t grid, i
 // a fit to some 300 measured combinations on a B200 (within 20%): 4.4 for a
 // launch, 2.7 for a joined reduction, 3.8 for each further round of resident
 // CTAs, and for each CTA of the busiest SM 0.16 a stage of 64 steps plus 0.27
-// by its columns (of 256), and 6.3 by its columns to finish them.  Clusters of
+// by its columns (of 256), and 6.3 by its columns to finish them (16 where the
+// output's rows are not whole vectors).  Clusters of
 // four and eight CTAs, an SM each, find room for fewer (in whole groups of
 // SMs).
 struct TilePlan {
@@ -115,7 +116,7 @@ struct TilePlan {
     double us;
 };
 TilePlan plan_tiles(const Product &p, int sms) {
-    const bool swap = p.swap();
+    const bool swap = p.swap(), vec = vector_rows(p);
     const int64_t rows = ceil_div(swap ? p.features : p.tokens, kLinRows), cols = swap ? p.tokens : p.features;
     TilePlan best{0, 0, 0, 1e300};
     for (int bn = 256; bn >= 32; bn /= 2) {
@@ -133,15 +134,18 @@ TilePlan plan_tiles(const Product &p, int sms) {
             const int64_t rounds = t.bn <= 64 ? ceil_div(on_sm, 2) : on_sm;   // two narrow tiles share an SM
             const double wide = t.bn / 256.0;
             t.us = 4.4 + (t.splits > 1 ? 2.7 : 0.0) + (rounds - 1) * 3.8 +
-                   on_sm * (kb * (0.16 + 0.27 * wide) + 6.3 * wide / t.splits);
+                   on_sm * (kb * (0.16 + 0.27 * wide) + (vec ? 6.3 : 16.0) * wide / t.splits);
             if (t.us < best.us) best = t;
         }
     }
     return best;
 }
 
-// On CTA pairs: the busiest pair's 64-step blocks at 0.40 (256 columns) or 0.32,
-// the launch and the last tile's output.
+// On CTA pairs: the launch at 5.6, and for the busiest pair either its 64-step
+// blocks at 0.40 (256 columns) or 0.32 and the last tile's output, or all of
+// its tiles' outputs after the first one's blocks, whichever takes longer.  A
+// tile's output takes 4.7 or 2.8, 10.4 or 6.2 where the rows are not whole
+// vectors.
 struct PairPlan {
     int32_t bn;
     double us;
@@ -162,13 +166,17 @@ PairPlan plan_pairs(const Product *const *p, int count, int pairs) {
         const int64_t kb0 = p[0]->kblocks(), kb1 = count > 1 ? p[1]->kblocks() : 1;
         int32_t early, late_from;
         deal(t0, t1, kb0, kb1, pairs, early, late_from);
-        int64_t most = 0;
+        const double block = bn == 256 ? 0.40 : 0.32;
+        const auto output = [bn](const Product &p) { return vector_rows(p) ? 0.9 + bn / 68.0 : 2.0 + bn / 30.5; };
+        const double e0 = output(*p[0]), e1 = count > 1 ? output(*p[1]) : e0;
+        double us = 0.0;
         for (int c = 0; c < pairs; ++c) {
             const int64_t rest = t1 - int64_t(early) * (pairs - late_from);
-            const int64_t n0 = (t0 - c + pairs - 1) / pairs, n1 = (rest - c + pairs - 1) / pairs;
-            most = std::max(most, n0 * kb0 + ((c >= late_from ? early : 0) + n1) * kb1);
+            const int64_t n0 = (t0 - c + pairs - 1) / pairs;
+            const int64_t n1 = (rest - c + pairs - 1) / pairs + (c >= late_from ? early : 0);
+            us = std::max({us, (n0 * kb0 + n1 * kb1) * block + e1, n0 * e0 + n1 * e1 + kb0 * block});
         }
-        const double us = 4.5 + most * (bn == 256 ? 0.40 : 0.32) + bn / 85.0;
+        us += 5.6;
         if (us < best.us) best = PairPlan{bn, us};
     }
     return best;

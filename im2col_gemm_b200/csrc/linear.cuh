@@ -139,9 +139,10 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, f
 
 // A CTA's share of a tile: `rows` tokens from m0 on, `width` features from n0
 // on, summed from the SPLITS partial copies [rows_all][ld] in its shared memory
-// in order, finished and stored.  VEC: eight features a thread, 16-byte stores
-// (a warp's store of 32 single elements takes the load-store unit as long as
-// one of 32 vectors); else one feature a lane, four tokens at a time.
+// in order, finished and stored, eight features a thread.  VEC: the rows are
+// whole 16-byte vectors; else they are cut at the 16-byte boundaries of y, and
+// the ends stored as single elements.  (One feature a lane: 1024 x 1023 x 64
+// took 11 us, now 8.8; with a branch around each element's loads 15.)
 template <typename T, int SPLITS, bool VEC>
 __device__ __forceinline__ void tile_epilogue(const LinParams &P, const float *part, int ld, int rows_all, int rows,
                                               int width, int64_t m0, int n0) {
@@ -180,30 +181,54 @@ __device__ __forceinline__ void tile_epilogue(const LinParams &P, const float *p
         }
         return;
     }
-    constexpr int U = 4;
+    // a warp: eight rows, four runs of each
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int n = lane; n < width; n += 32) {
-        const float bias = P.bias ? __ldg(P.bias + n0 + n) : 0.f;
-        for (int o = warp * U; o < rows; o += kLinThreads / 32 * U) {
-            float r[U], s[U];
+    const int across = ((width + 14) / 8 + 3) / 4, items = (rows + 7) / 8 * across;
+    const bool z_alike = ((P.ldz ^ P.ldy) & 7) == 0, res_alike = ((P.ldr ^ P.ldy) & 7) == 0;
+    for (int it = warp; it < items; it += kLinThreads / 32) {
+        const int o = it / across * 8 + lane / 4;
+        const int64_t m = m0 + o;
+        const int n = (it % across * 4 + lane % 4) * 8 - static_cast<int>((m * P.ldy + n0) & 7);
+        if (o >= rows || n >= width) continue;
+        const int lo = max(0, -n), hi = min(8, width - n);
+        const bool whole = lo == 0 && hi == 8;
+        T *to = y + m * P.ldy + n0 + n;
+        // what lies outside reads its neighbour's: no branches between the loads
+        float v[8], f[8] = {};
+        int at[8];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                r[u] = res && o + u < rows ? to_f32(res[(m0 + o + u) * P.ldr + n0 + n]) : 0.f;
+        for (int q = 0; q < 8; ++q) at[q] = min(max(n + q, 0), width - 1);
+        if (res && whole && res_alike) {
+            Vec<T>::widen(*reinterpret_cast<const uint4 *>(res + m * P.ldr + n0 + n), f);
+        } else if (res) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                s[u] = 0.f;
-                if (o + u < rows) {
-                    s[u] = part[(o + u) * ld + n];
+            for (int q = 0; q < 8; ++q) f[q] = to_f32(res[m * P.ldr + n0 + at[q]]);
+        }
 #pragma unroll
-                    for (int c = 1; c < SPLITS; ++c) s[u] += part[(c * rows_all + o + u) * ld + n];
-                    s[u] += bias;
-                    if (z) z[(m0 + o + u) * P.ldz + n0 + n] = from_f32<T>(s[u]);
-                }
-            }
-            act_values(P.act, s);
+        for (int q = 0; q < 8; ++q) v[q] = part[o * ld + at[q]];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (o + u < rows) y[(m0 + o + u) * P.ldy + n0 + n] = from_f32<T>(res ? s[u] + r[u] : s[u]);
+        for (int c = 1; c < SPLITS; ++c)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += part[(c * rows_all + o) * ld + at[q]];
+        if (P.bias) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] += __ldg(P.bias + n0 + at[q]);
+        }
+        if (z && whole && z_alike) {
+            *reinterpret_cast<uint4 *>(z + m * P.ldz + n0 + n) = Vec<T>::narrow(v);
+        } else if (z) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q >= lo && q < hi) z[m * P.ldz + n0 + n + q] = from_f32<T>(v[q]);
+        }
+        act_values(P.act, v);
+        if (res) add_to(v, f);
+        if (whole) {
+            *reinterpret_cast<uint4 *>(to) = Vec<T>::narrow(v);
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q >= lo && q < hi) to[q] = from_f32<T>(v[q]);
         }
     }
 }
@@ -528,7 +553,7 @@ struct PairEpilogue {
     // number, so that neither side meets bank conflicts), and a warp writes 32
     // features of one token at a time.  (64 features in 4-byte words took
     // longer: the odd rows' ends need stores of their own.)
-    __device__ __forceinline__ void block_any(const uint32_t (&acc)[32], int64_t m0, int n) {
+    __device__ __forceinline__ void block_any(const uint32_t (&acc)[32], float bias, int64_t m0, int n) {
         float *f = reinterpret_cast<float *>(buf);
         if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
@@ -537,7 +562,6 @@ struct PairEpilogue {
         __syncwarp();
         if (n + lane >= P.J) return;
         const int rows = static_cast<int>(min(static_cast<int64_t>(32), P.I - m0));
-        const float bias = P.bias ? __ldg(P.bias + n + lane) : 0.f;
         const T *res = P.res ? static_cast<const T *>(P.res) + m0 * P.ldr + n + lane : nullptr;
         T *y = static_cast<T *>(P.y) + m0 * P.ldy + n + lane;
         T *z = P.z ? static_cast<T *>(P.z) + m0 * P.ldz + n + lane : nullptr;
@@ -764,6 +788,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
             if (!mbar_wait(&acc_full[b], (n >> 1) & 1, kLinTimeoutNs, abort)) break;
             tc_fence_after();
             for (int c = 0; c < bn / 2; c += 32) {
+                const int mine = j0 + c + lane;   // block_any's column, asked for before the accumulators
+                const float bias = !P.vec_out && P.bias && mine < P.J ? __ldg(P.bias + mine) : 0.f;
                 uint32_t acc[32];
                 tc_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + b * bn + half * (bn / 2) + c,
                                  acc);
@@ -780,7 +806,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
                     if (P.res && !last) out.fetch(r, i0 + lane, j0 + c + 32);
                     out.block(acc, now, i0, j0 + c);
                 } else {
-                    out.block_any(acc, i0, j0 + c);
+                    out.block_any(acc, bias, i0, j0 + c);
                 }
             }
         }
