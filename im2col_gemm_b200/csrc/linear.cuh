@@ -141,8 +141,9 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, f
 // on, summed from the SPLITS partial copies [rows_all][ld] in its shared memory
 // in order, finished and stored, eight features a thread.  VEC: the rows are
 // whole 16-byte vectors; else they are cut at the 16-byte boundaries of y, and
-// the ends stored as single elements.  (One feature a lane: 1024 x 1023 x 64
-// took 11 us, now 8.8; with a branch around each element's loads 15.)
+// the ends stored as single elements.  (Both gradients of 509 x 777 x 1003: one
+// feature a lane 18.4 us, with a branch around each element's loads 20.5, now
+// 14.1.)
 template <typename T, int SPLITS, bool VEC>
 __device__ __forceinline__ void tile_epilogue(const LinParams &P, const float *part, int ld, int rows_all, int rows,
                                               int width, int64_t m0, int n0) {
@@ -181,15 +182,13 @@ __device__ __forceinline__ void tile_epilogue(const LinParams &P, const float *p
         }
         return;
     }
-    // a warp: eight rows, four runs of each
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int across = ((width + 14) / 8 + 3) / 4, items = (rows + 7) / 8 * across;
+    const int across = (width + 14) / 8;   // the most runs of a row
     const bool z_alike = ((P.ldz ^ P.ldy) & 7) == 0, res_alike = ((P.ldr ^ P.ldy) & 7) == 0;
-    for (int it = warp; it < items; it += kLinThreads / 32) {
-        const int o = it / across * 8 + lane / 4;
+    for (int e = threadIdx.x; e < rows * across; e += kLinThreads) {
+        const int o = e / across;
         const int64_t m = m0 + o;
-        const int n = (it % across * 4 + lane % 4) * 8 - static_cast<int>((m * P.ldy + n0) & 7);
-        if (o >= rows || n >= width) continue;
+        const int n = (e - o * across) * 8 - static_cast<int>((m * P.ldy + n0) & 7);
+        if (n >= width) continue;
         const int lo = max(0, -n), hi = min(8, width - n);
         const bool whole = lo == 0 && hi == 8;
         T *to = y + m * P.ldy + n0 + n;
@@ -242,9 +241,9 @@ __device__ __forceinline__ void tile_epilogue(const LinParams &P, const float *p
 // it got in rank order and stores it.  So a product with few tiles uses all
 // SMs in one launch, without a workspace, and gives the same bits each time.
 // Small products are bound by latency: a launch, the first stages, a barrier
-// for the join, the epilogue.  128 x 1003 x 515 fp16 takes 10.7 us with the
+// for the join, the epilogue.  128 x 1003 x 515 fp16 takes 9.6 us with the
 // copies of both operands before it, where its 1.4 MB would take 0.2; both
-// gradients of 509 x 777 x 1003 19 us with the copies and dz.
+// gradients of 509 x 777 x 1003 14.1 us with the copies and dz.
 template <typename T>
 __global__ void __launch_bounds__(kLinThreads) linear_tile_kernel(const __grid_constant__ LinGroup G) {
     extern __shared__ uint8_t lin_smem_raw[];
