@@ -297,3 +297,26 @@ def test_helper_refusals(mqc):
         mqc.linear_fwd(t["x"].float(), t["w"].float())
     with pytest.raises(mqc.MqcError):       # overlapping rows
         mqc.linear_fwd(t["x"][:1].expand(8, 24), t["w"])
+
+
+@pytest.mark.parametrize("shape", [(1, 203, 72), (40, 203, 512), (130, 203, 72), (300, 1003, 130), (2000, 2045, 64)])
+@pytest.mark.parametrize("strides", [(5, 1, 2), (5, 13, 21), (0, 0, 0), (3, 11, 0)])
+def test_rows_that_start_anywhere(mqc, shape, strides):
+    """y, z and the residual with row strides of their own, alike modulo 16
+    bytes or not: pieces of rows are stored whole where they can be, and
+    nothing between the rows is touched."""
+    m, n, k = shape
+    ldy, ldz, ldr = (n + s for s in strides)
+    t = make(m, n, k, F16, seed=n)
+    y, z, r = (torch.full((m, ld), 7.0, dtype=F16, device="cuda") for ld in (ldy, ldz, ldr))
+    r[:, :n] = t["residual"]
+    lin = mqc.Linear(m, n, k, mqc.F16, 2, k, k, ldr, ldy, ldz, n, k, k)
+    ws = torch.empty(max(1, mqc.lib.mqc_linear_fwd_workspace_bytes(lin)), dtype=torch.uint8, device="cuda")
+    mqc.check(mqc.lib.mqc_linear_fwd(lin, t["x"].data_ptr(), t["w"].data_ptr(), t["bias"].data_ptr(), r.data_ptr(),
+                                     y.data_ptr(), z.data_ptr(), ws.data_ptr(), ws.numel(),
+                                     torch.cuda.current_stream().cuda_stream))
+    mqc.check(mqc.get_device_status())
+    wy, wz, ey, ez = ref.linear_fwd(t["x"], t["w"], t["bias"], 2, t["residual"])
+    near(y[:, :n], wy, ey, F16)
+    near(z[:, :n], wz, ez, F16)
+    assert (y[:, n:] == 7).all() and (z[:, n:] == 7).all()
