@@ -623,10 +623,17 @@ def _row_stride(t, rows: int, cols: int) -> int:
         return cols
     if t.shape != (rows, cols):
         raise ValueError(f"expected shape {(rows, cols)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return cols
     row, col = t.stride()
     if col != 1 and cols > 1:
         raise ValueError("the elements of a row must be contiguous")
     return row if rows > 1 else max(cols, row)
+
+
+def _like(t, rows: int, cols: int):
+    """A new contiguous matrix of t's shape and type."""
+    return _torch().empty_like(t) if t.is_contiguous() else t.new_empty((rows, cols))
 
 
 def _linear_sizes(name: str, x, w) -> tuple[int, int, int]:
@@ -644,7 +651,7 @@ def linear_fwd(x, w, bias=None, act: int = ACT_NONE, residual=None, save_z: bool
     _same(x, w, residual, out)
     _params(x, n, bias)
     y = out if out is not None else x.new_empty((m, n))
-    z = x.new_empty((m, n)) if save_z else None
+    z = None if not save_z else _torch().empty_like(y) if out is None else x.new_empty((m, n))
     lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, m, k), _row_stride(w, n, k), _row_stride(residual, m, n),
                  _row_stride(out, m, n), n, n, k, k)
     ws, at, nws = _scratch(lib.mqc_linear_fwd_workspace_bytes(lin), x, workspace)
@@ -661,8 +668,8 @@ def linear_bwd(g, x, w, z=None, act: int = ACT_NONE, need_x: bool = True, need_w
     None."""
     m, n, k = _linear_sizes("linear_bwd", x, w)
     _same(g, x, w, z)
-    gx = x.new_empty((m, k)) if need_x else None
-    gw = x.new_empty((n, k)) if need_w else None
+    gx = _like(x, m, k) if need_x else None
+    gw = _like(w, n, k) if need_w else None
     gb = x.new_empty(n, dtype=_torch().float32) if need_bias else None
     lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, m, k), _row_stride(w, n, k), n, n, _row_stride(z, m, n),
                  _row_stride(g, m, n), k, k)

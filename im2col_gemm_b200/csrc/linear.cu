@@ -170,10 +170,10 @@ PairPlan plan_pairs(const Product *const *p, int count, int pairs) {
         const auto output = [bn](const Product &p) { return vector_rows(p) ? 0.9 + bn / 68.0 : 2.0 + bn / 30.5; };
         const double e0 = output(*p[0]), e1 = count > 1 ? output(*p[1]) : e0;
         double us = 0.0;
-        for (int c = 0; c < pairs; ++c) {
-            const int64_t rest = t1 - int64_t(early) * (pairs - late_from);
-            const int64_t n0 = (t0 - c + pairs - 1) / pairs;
-            const int64_t n1 = (rest - c + pairs - 1) / pairs + (c >= late_from ? early : 0);
+        const int64_t rest = t1 - int64_t(early) * (pairs - late_from);
+        const int64_t each0 = t0 / pairs, each1 = rest / pairs, more1 = rest % pairs;
+        for (int64_t c : {int64_t(0), int64_t(late_from), more1}) {   // where the pairs' shares change
+            const int64_t n0 = each0 + (c < late_from), n1 = each1 + (c < more1) + (c >= late_from ? early : 0);
             us = std::max({us, (n0 * kb0 + n1 * kb1) * block + e1, n0 * e0 + n1 * e1 + kb0 * block});
         }
         us += 5.6;
