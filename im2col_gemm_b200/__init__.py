@@ -637,9 +637,10 @@ def _like(t, rows: int, cols: int):
 
 
 def _linear_sizes(name: str, x, w) -> tuple[int, int, int]:
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
-        raise ValueError(f"{name} takes x [M][K] and w [N][K], got {tuple(x.shape)} and {tuple(w.shape)}")
-    return x.shape[0], w.shape[0], x.shape[1]
+    xs, ws = x.shape, w.shape
+    if len(xs) != 2 or len(ws) != 2 or xs[1] != ws[1]:
+        raise ValueError(f"{name} takes x [M][K] and w [N][K], got {tuple(xs)} and {tuple(ws)}")
+    return xs[0], ws[0], xs[1]
 
 
 @_on_device
@@ -652,7 +653,8 @@ def linear_fwd(x, w, bias=None, act: int = ACT_NONE, residual=None, save_z: bool
     _params(x, n, bias)
     y = out if out is not None else x.new_empty((m, n))
     z = None if not save_z else _torch().empty_like(y) if out is None else x.new_empty((m, n))
-    lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, m, k), _row_stride(w, n, k), _row_stride(residual, m, n),
+    lin = Linear(m, n, k, _dtype(x), act, k if x.is_contiguous() else _row_stride(x, m, k),
+                 k if w.is_contiguous() else _row_stride(w, n, k), _row_stride(residual, m, n),
                  _row_stride(out, m, n), n, n, k, k)
     ws, at, nws = _scratch(lib.mqc_linear_fwd_workspace_bytes(lin), x, workspace)
     check(lib.mqc_linear_fwd(lin, x.data_ptr(), w.data_ptr(), _address(bias), _address(residual), y.data_ptr(),
@@ -671,7 +673,8 @@ def linear_bwd(g, x, w, z=None, act: int = ACT_NONE, need_x: bool = True, need_w
     gx = _like(x, m, k) if need_x else None
     gw = _like(w, n, k) if need_w else None
     gb = x.new_empty(n, dtype=_torch().float32) if need_bias else None
-    lin = Linear(m, n, k, _dtype(x), act, _row_stride(x, m, k), _row_stride(w, n, k), n, n, _row_stride(z, m, n),
+    lin = Linear(m, n, k, _dtype(x), act, k if x.is_contiguous() else _row_stride(x, m, k),
+                 k if w.is_contiguous() else _row_stride(w, n, k), n, n, _row_stride(z, m, n),
                  _row_stride(g, m, n), k, k)
     ws, at, nws = _scratch(lib.mqc_linear_bwd_workspace_bytes(lin), x, workspace)
     check(lib.mqc_linear_bwd(lin, g.data_ptr(), _address(z), x.data_ptr(), w.data_ptr(), _address(gx), _address(gw),
