@@ -835,8 +835,8 @@ __global__ void __launch_bounds__(kGnThreads) gn_chip_fwd_kernel(const __grid_co
             const bool in = lane < P.splits;
             const float n = in ? static_cast<float>(min(P.HW - lane * P.slab, P.slab)) * P.D : 0.f;
             const float mr = in ? gn_ld_rank(sums + g, lane) : 0.f, sr = in ? gn_ld_rank(dev + g, lane) : 0.f;
-            // about the first CTA's mean, so that equal means stay exact
-            const float base = __shfl_sync(0xFFFFFFFFu, mr, 0);
+            // about the first CTA's mean (0 if that is not finite), so that equal means stay exact
+            const float head = __shfl_sync(0xFFFFFFFFu, mr, 0), base = isfinite(head) ? head : 0.f;
             mu = base + warp_sum_f(in ? n * (mr - base) : 0.f, 8) / total;
             mu = __shfl_sync(0xFFFFFFFFu, mu, 0);
             s2 = warp_sum_f(in ? fmaf(n * (mr - mu), mr - mu, sr) : 0.f, 8);

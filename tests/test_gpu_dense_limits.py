@@ -69,3 +69,29 @@ def test_silu_far_below_zero_backward(mqc, shape, dtype):
         t["beta"][2 * i + 1] = low
     t["beta"][24:27] = torch.tensor([-1e30, -1e20, 60.0])
     check_bwd(mqc, t, groups, 2)
+
+
+# One CTA, a cluster of four (on chip: no workspace), two passes.
+@pytest.mark.parametrize("where", [0.0, 0.5, 1.0])
+@pytest.mark.parametrize("value", [INF, -INF])
+@pytest.mark.parametrize("shape,dtype", [((2, 128, 6, 6, 32), BF16), ((8, 128, 80, 80, 32), BF16),
+                                         ((1, 64, 180, 180, 32), F32)])
+def test_an_infinity_leaves_an_infinite_mean(mqc, shape, dtype, value, where):
+    """In whichever part of the image it lies; the outputs of its group are
+    NaN, and the other groups keep their bits."""
+    n, c, h, w, groups = shape
+    t = make(n, c, h, w, dtype, seed=3)
+    xd = mqc.T4(n, c, h, w, *t["x"].stride())
+    code = mqc.F32 if dtype == F32 else mqc.BF16
+    assert (mqc.mqc_group_norm_fwd_workspace_bytes(xd, xd, code, groups) == 0) == (h != 180)
+    clean = mqc.group_norm_fwd(t["x"], groups, t["gamma"], t["beta"], EPS, 2)
+    x = t["x"].clone(memory_format=torch.channels_last)
+    per = c // groups
+    x[n - 1, 2 * per, round(where * (h - 1)), round(where * (w - 1))] = value
+    y, mean, rstd = mqc.group_norm_fwd(x, groups, t["gamma"], t["beta"], EPS, 2)
+    hit = torch.zeros(n, groups, dtype=torch.bool)
+    hit[n - 1, 2] = True
+    assert mean[hit].item() == value and torch.isnan(rstd[hit]).all()
+    assert torch.equal(mean[~hit], clean[1][~hit]) and torch.equal(rstd[~hit], clean[2][~hit])
+    hit = hit.repeat_interleave(per, 1)
+    assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], clean[0][~hit])
