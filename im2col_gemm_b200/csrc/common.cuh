@@ -231,8 +231,11 @@ __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t adesc, uin
 }
 
 // 32 lanes x 16 consecutive 32-bit columns: thread i of the warp receives
-// lane (base lane + i), columns col .. col+15.
+// lane (base lane + i), columns col .. col+15.  The whole warp executes these
+// loads together, so its lanes meet first: they come from waits and from the
+// last columns' stores, which are not the same for all of them.
 __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
         "%14, %15}, [%16];"
@@ -244,6 +247,7 @@ __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[1
 
 // As above, into r[0..15] of a longer array.
 __device__ __forceinline__ void tc_ld_32x32b_x16p(uint32_t taddr, uint32_t *r) {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
         "%14, %15}, [%16];"
@@ -255,6 +259,7 @@ __device__ __forceinline__ void tc_ld_32x32b_x16p(uint32_t taddr, uint32_t *r) {
 
 // 32 lanes x 32 consecutive 32-bit columns.
 __device__ __forceinline__ void tc_ld_32x32b_x32(uint32_t taddr, uint32_t *r) {
+    __syncwarp();
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
         "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"

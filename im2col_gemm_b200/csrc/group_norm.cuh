@@ -699,10 +699,13 @@ __device__ __forceinline__ float gn_ld_rank(const float *p, uint32_t rank) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
+// (The lanes of a warp come from loops and branches of their own.)
 __device__ __forceinline__ void gn_cluster_arrive() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void gn_cluster_wait() {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t gn_cluster_id() {

@@ -103,6 +103,7 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t map_to_rank(uint32_t saddr, uint32_t rank) {
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
             j0 += half * (bn / 2);
             uint4 r[4];
             if (P.res && P.vec_out) out.fetch(r, i0 + lane, j0);
-            if (!mbar_wait(&acc_full[b], (n >> 1) & 1, kLinTimeoutNs, abort)) break;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[b], (n >> 1) & 1, kLinTimeoutNs, abort))) break;
             tc_fence_after();
             for (int c = 0; c < bn / 2; c += 32) {
                 const int mine = j0 + c + lane;   // block_any's column, asked for before the accumulators

@@ -214,3 +214,24 @@ def test_workspace_of_another_device_or_with_gaps_is_refused(mqc):
     with pytest.raises(ValueError, match="workspace"):
         mqc._scratch(64, host, host[::2])
     assert mqc._scratch(64, host, host)[2] == 128
+
+
+def test_warps_meet_before_instructions_that_they_execute_together():
+    """Cluster barriers and loads from tensor memory of the .aligned form are
+    undefined unless all lanes of a warp arrive together, and callers reach
+    them from loops and branches that differ by lane: each wrapper brings the
+    lanes together itself."""
+    import glob
+    import os
+    import re
+    here = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    files = sorted(glob.glob(os.path.join(here, "im2col_gemm_b200", "csrc", "*.cu*")))
+    found = []
+    for path in files:
+        with open(path) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"asm volatile\(\s*\"(barrier\.cluster\.\S*\.aligned|tcgen05\.ld\.sync\.aligned)", text):
+            before = text[:m.start()].rstrip()
+            found.append((os.path.basename(path), m.group(1), before.endswith("__syncwarp();")))
+    assert len(found) >= 6
+    assert all(ok for _, _, ok in found), [f for f in found if not f[2]]
