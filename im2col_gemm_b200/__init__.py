@@ -488,10 +488,11 @@ _CUDA: dict = {}
 
 def _setup() -> None:
     torch = _torch()
-    _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _CUDA["stream"] = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
     _CUDA["count"] = torch.cuda.device_count()
+    # last, and at once: other threads take it as the sign that all is there
+    _DTYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16})
 
 
 def _on_device(fn):

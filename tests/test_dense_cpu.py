@@ -235,3 +235,39 @@ def test_warps_meet_before_instructions_that_they_execute_together():
             found.append((os.path.basename(path), m.group(1), before.endswith("__syncwarp();")))
     assert len(found) >= 6
     assert all(ok for _, _, ok in found), [f for f in found if not f[2]]
+
+
+def test_a_second_thread_during_the_first_call(mqc, monkeypatch):
+    """The first call looks things up; a second thread whose first call falls
+    into that finds all of them or looks them up itself."""
+    import threading
+
+    class OnDevice:   # what the wrapper looks at
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
+    @mqc._on_device
+    def call(t):
+        return "ran"
+
+    results = []
+
+    def second():
+        try:
+            results.append(call(OnDevice()))
+        except Exception as e:
+            results.append(e)
+
+    def device_count():   # releases the interpreter lock
+        if threading.current_thread() is threading.main_thread():
+            thread = threading.Thread(target=second)
+            thread.start()
+            thread.join()
+        return 1
+
+    for table in ("_DTYPES", "_CUDA"):
+        monkeypatch.setattr(mqc, table, {})
+    monkeypatch.setattr(torch.cuda, "device_count", device_count)
+    assert call(OnDevice()) == "ran" and results == ["ran"]
