@@ -143,7 +143,7 @@ mqc_status dropout(const char *name, const void *x, int64_t ldx, const void *res
         return fail(MQC_ERR_ALIGNMENT, "%s: tensor not 16-byte aligned", name);
     if ((reinterpret_cast<uintptr_t>(offset_dev) & 7u) != 0)
         return fail(MQC_ERR_ALIGNMENT, "%s: offset_dev not 8-byte aligned", name);
-    if ((y == x && ldx != ldy) || (res && y == res && ldr != ldy))
+    if (rows > 1 && ((y == x && ldx != ldy) || (res && y == res && ldr != ldy)))
         return fail(MQC_ERR_INVALID, "%s: an output in place needs its input's row stride", name);
     DeviceLimits d;
     mqc_status st = device_limits(&d);

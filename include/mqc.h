@@ -478,7 +478,7 @@ MQC_API size_t mqc_linear_bwd_workspace_bytes(const mqc_linear *lin);
  * high).
  *   x, y, residual   [rows][cols] of `dtype`, row strides ldx, ldy, ldr in
  *           elements; residual may be NULL.  y may be x or residual itself
- *           (same stride).
+ *           (same stride, where there is more than one row).
  *   offset  plus, when offset_dev is not NULL, the device value *offset_dev
  *           (8-byte aligned, read when the kernel runs): a captured graph
  *           draws new bits at every replay when the program advances it.

@@ -150,3 +150,17 @@ def test_helper_refusals(mqc):
             call()
     with pytest.raises(TypeError):
         mqc.dropout_fwd(x.double(), 0.5, 1)
+
+
+@pytest.mark.parametrize("which", ["x", "residual"])
+def test_one_row_in_place_whatever_its_strides(mqc, which):
+    """A single row has no next one: its strides may differ in place too."""
+    n, seed = 1003, 77
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x, r = (torch.randn(1, n, generator=gen, device="cuda") for _ in range(2))
+    want = mqc.dropout_fwd(x, 0.25, seed, residual=r)
+    y = x if which == "x" else r
+    lds = (n + 5, n) if which == "x" else (n, n + 5)
+    mqc.check(mqc.mqc_dropout_fwd(x.data_ptr(), lds[0], r.data_ptr(), lds[1], 1, n, mqc.F32, 0.25, seed, 0, None,
+                                  y.data_ptr(), n, torch.cuda.current_stream().cuda_stream))
+    assert torch.equal(y, want)
