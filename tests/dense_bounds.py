@@ -4,7 +4,13 @@ many pixels.
 
 - The activations' errors are relative to their values.  SiLU is z q with q
   from a fast exponential and reciprocal: the exponent's rounding, |z| U, and a
-  few steps more, and 0 where q is below the normal numbers.
+  few steps more, and 0 where q is below the normal numbers.  GELU's normal
+  distribution is P(t) exp(-z^2 / 2) below 0 and 1 minus that above: 2 U for the
+  fit and its coefficients, 5 U for the evaluation of P, 6 U for t (a fused
+  multiplication and a fast reciprocal, weighed by t P'/P <= 2), 4 U for the
+  fast exponential, U for the product, and 1.5 z^2 U for the exponent's three
+  roundings: (20 + 2 z^2) U of it; 0 where the exponential is below the normal
+  numbers.
 - Sums follow the longest chain of fp32 additions that the kernels have: `run`
   values that one thread adds up, and JOIN additions across the block (a
   thread's own channels, the rows of a block in turn, a warp's lanes); slabs
@@ -22,12 +28,20 @@ U = ref.U
 JOIN = 48
 
 
+def gelu_tail(z):
+    """The normal distribution at -|z|, and what of it is flushed to 0."""
+    tail = 0.5 * torch.special.erfc(z.abs() / 2 ** 0.5)
+    return tail, torch.where(z.abs() > 13, tail, 0.0)
+
+
 def act_error(z, a):
     """Error of act evaluated in fp32 at an exact z."""
     if a in (NONE, RELU):
         return torch.zeros_like(z)
     if a == GELU:
-        return ref.act_error(z, a)
+        tail, lost = gelu_tail(z)
+        return z.abs() * (tail * ((20 + 2 * z * z) * U).clamp(max=1.0) + lost + U) * (z > 0) + (
+            ref.act(z, a).abs() * ((21 + 2 * z * z) * U).clamp(max=1.0) + z.abs() * lost) * (z <= 0)
     y = ref.act(z, a).abs()
     return y * ((8 + 2 * z.abs()) * U).clamp(max=1.0) + torch.where(z < -86, y, 0.0)
 
@@ -37,7 +51,9 @@ def slope_error(z, a):
     if a in (NONE, RELU):
         return torch.zeros_like(z)
     if a == GELU:
-        return ref.slope_error(z, a)
+        tail, lost = gelu_tail(z)
+        bell = z.abs() * torch.exp(-z * z / 2) * (2 * torch.pi) ** -0.5
+        return (tail + bell) * ((22 + 2 * z * z) * U).clamp(max=1.0) + lost * (1 + z.abs()) ** 2 + 2 * U * (z > 0)
     q = torch.sigmoid(z)
     return q * (1 + z.abs()) * ((8 + 2 * z.abs()) * U).clamp(max=1.0) + torch.where(z < -86, q * (1 + z.abs()), 0.0)
 
@@ -59,7 +75,7 @@ def slope_spread(z, e, a):
     if a == RELU:   # a sign that the error of z may flip
         return (z.abs() <= e).double()
     tail = ref.slope(-(z.abs() - e), a).abs()
-    near = torch.where(z.abs() < 10, ref.CURVE[a] * e, 1.2 * tail * e)
+    near = torch.where(z.abs() < 10, ref.CURVE[a] * e, (2 + z.abs() if a == GELU else 1.2) * tail * e)
     return torch.where(e < 0.01, near, torch.where(z.abs() - e > 20, tail, 2.2))
 
 

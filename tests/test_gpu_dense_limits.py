@@ -1,6 +1,7 @@
-"""Group norm where its values, sums or statistics run to their limits, against
+"""Dense layers where their values, sums or statistics run to their limits, against
 the 64-bit form within bounds that stay below the values (dense_bounds)."""
 import dense_bounds as tight
+import dense_ref as ref
 import pytest
 import torch
 
@@ -95,3 +96,75 @@ def test_an_infinity_leaves_an_infinite_mean(mqc, shape, dtype, value, where):
     assert torch.equal(mean[~hit], clean[1][~hit]) and torch.equal(rstd[~hit], clean[2][~hit])
     hit = hit.repeat_interleave(per, 1)
     assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], clean[0][~hit])
+
+
+# z is given exactly: beta where a group has no spread, the bias where x is 0.
+Z = {2: (-110.0, 30.0), 3: (-14.0, 9.0)}
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("pixels", [1, 40000])
+@pytest.mark.parametrize("act", [2, 3])
+def test_group_norm_activations_at_given_values(mqc, act, pixels, dtype):
+    """act and act' themselves, relative to their values, over all that is not
+    yet 0 or z: in groups of equal values z is beta, and where there is one
+    pixel gbeta is g act'(beta)."""
+    c, side = 4096 if pixels == 1 else 64, int(pixels ** 0.5)
+    beta = torch.linspace(*Z[act], c, device="cuda")
+    x = torch.full((1, side, side, c), 3.25, dtype=dtype, device="cuda").permute(0, 3, 1, 2)
+    y, mean, rstd = mqc.group_norm_fwd(x, c // 8, None, beta, EPS, act)
+    assert (mean == 3.25).all()
+    z = beta.double().view(1, c, 1, 1).expand(x.shape)
+    within(y, ref.act(z, act), tight.act_error(z, act) + U_Y * ref.act(z, act).abs(), "y")
+    if pixels == 1:
+        g = make(1, c, 1, 1, dtype)["g"]
+        got = mqc.group_norm_bwd(g, x, c // 8, mean, rstd, None, beta, act)[2]
+        s, gd = ref.slope(beta.double(), act), g.double().view(c)
+        within(got, gd * s, gd.abs() * (tight.slope_error(beta.double(), act) + U_Y * s.abs()), "gbeta")
+
+
+U_Y = 2 * ref.U   # a product's rounding, and the sums' that follow
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("m,n", [(1, 4096), (40, 2048), (129, 1003), (3000, 4096)])
+@pytest.mark.parametrize("act", [2, 3])
+def test_linear_activations_at_given_values(mqc, act, m, n, dtype):
+    """The same for the linear layer: x = 0 leaves z = bias, and with one token
+    gb is g act'(z)."""
+    bias = torch.linspace(*Z[act], n, device="cuda")
+    x, w = torch.zeros(m, 64, dtype=dtype, device="cuda"), torch.ones(n, 64, dtype=dtype, device="cuda")
+    y, z = mqc.linear_fwd(x, w, bias, act, save_z=True)
+    mqc.check(mqc.get_device_status())
+    assert torch.equal(z, bias.to(dtype).expand(m, n))
+    exact = bias.double().expand(m, n)
+    within(y, ref.act(exact, act), tight.act_error(exact, act) + U_Y * ref.act(exact, act).abs(), "y")
+    if m == 1:
+        g = make(1, n, 1, 1, dtype)["g"].reshape(1, n)
+        gb = mqc.linear_bwd(g, x, w, z, act)[2]
+        zd, gd = z.double().view(n), g.double().view(n)
+        s = ref.slope(zd, act)
+        within(gb, gd * s, gd.abs() * (tight.slope_error(zd, act) + U_Y * s.abs()), "gb")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", FAR)
+def test_gelu_over_its_range(mqc, shape, dtype):
+    *dims, groups = shape
+    t = make(*dims, dtype, seed=4)
+    t["beta"] = torch.linspace(-10.0, 8.0, dims[1], device="cuda")
+    y = mqc.group_norm_fwd(t["x"], groups, t["gamma"], t["beta"], EPS, 3)[0]
+    within(y, *tight.GroupNorm(t["x"], groups, t["gamma"], t["beta"], EPS, 3).forward(), "y")
+    check_bwd(mqc, t, groups, 3)
+
+
+def test_gelu_error_of_ordinary_values(mqc):
+    """fp32, standard normal z, as a 2-norm: a rounding of z, of the normal
+    distribution and of their product, U / sqrt 3 each on average, and half
+    again for the distribution's own evaluation (dense_bounds)."""
+    t = make(4, 64, 40, 40, F32, seed=5)
+    y, mean, rstd = mqc.group_norm_fwd(t["x"], 8, None, None, EPS, 3)
+    z = (t["x"].double() - mean.double().repeat_interleave(8, 1)[..., None, None]) * rstd.double().repeat_interleave(
+        8, 1)[..., None, None]
+    want = ref.act(z, 3)
+    assert ((y.double() - want).norm() / want.norm()).item() < 1.5 * ref.U
