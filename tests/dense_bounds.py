@@ -25,7 +25,26 @@ import torch
 
 NONE, RELU, SILU, GELU = 0, 1, 2, 3
 U = ref.U
+EPS = 1e-5
 JOIN = 48
+# Images that the two-pass form cuts into slabs, whose statistics and sums are
+# joined: 256 groups of one channel side by side, one group, groups of two, few
+# channels, several images.  A thread adds up 8 to 19 values of them, and no
+# more than 100 where an image stays on chip (200 KB for at least 128 threads).
+SLABS = [(1, 256, 180, 180, 256), (1, 64, 300, 300, 1), (2, 512, 60, 60, 256), (1, 8, 600, 600, 8),
+         (4, 64, 160, 160, 16), (1, 16, 200, 200, 4)]
+SLAB_PIXELS = [146, 203, 66, 1023, 231, 507]   # of one slab of each, fp32
+RUN = 100
+
+
+def make(n, c, h, w, dtype, seed=0, device="cpu", drift=False):
+    """Channels-last inputs; drift: a mean of 1000 that moves by 8 down the
+    image, so that the slabs have means of their own."""
+    gen = torch.Generator(device=device).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=gen, device=device)  # noqa: E731
+    last = lambda t: t.to(dtype).permute(0, 3, 1, 2)  # noqa: E731
+    x = r(n, h, w, c) + (torch.linspace(996.0, 1004.0, h, device=device).view(1, h, 1, 1) if drift else 0.5 * r(c))
+    return dict(x=last(x), g=last(r(n, h, w, c)), gamma=1 + 0.2 * r(c), beta=0.3 * r(c))
 
 
 def gelu_tail(z):

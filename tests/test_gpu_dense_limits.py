@@ -19,11 +19,8 @@ def mqc():
     return im2col_gemm_b200
 
 
-def make(n, c, h, w, dtype, seed=0):
-    gen = torch.Generator(device="cuda").manual_seed(seed)
-    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
-    last = lambda t: t.to(dtype).permute(0, 3, 1, 2)  # noqa: E731
-    return dict(x=last(r(n, h, w, c) + 0.5 * r(c)), g=last(r(n, h, w, c)), gamma=1 + 0.2 * r(c), beta=0.3 * r(c))
+def make(n, c, h, w, dtype, seed=0, drift=False):
+    return tight.make(n, c, h, w, dtype, seed, "cuda", drift)
 
 
 def within(got, want, bound, what):
@@ -168,3 +165,35 @@ def test_gelu_error_of_ordinary_values(mqc):
         8, 1)[..., None, None]
     want = ref.act(z, 3)
     assert ((y.double() - want).norm() / want.norm()).item() < 1.5 * ref.U
+
+
+def in_passes(mqc, t, groups):
+    """Whether the forward pass joins slabs: it needs a workspace then."""
+    xd = mqc.T4(*t["x"].shape, *t["x"].stride())
+    code = {F32: mqc.F32, F16: mqc.F16}[t["x"].dtype]
+    return mqc.mqc_group_norm_fwd_workspace_bytes(xd, xd, code, groups) > 0
+
+
+@pytest.mark.parametrize("dtype", [F32, F16])
+@pytest.mark.parametrize("shape", tight.SLABS)
+def test_sums_of_many_slabs(mqc, shape, dtype):
+    *dims, groups = shape
+    t = make(*dims, dtype, seed=groups)
+    assert in_passes(mqc, t, groups) or dims[3] == 200 or dtype == F16   # fewer bytes may stay on chip
+    y, mean, rstd = mqc.group_norm_fwd(t["x"], groups, t["gamma"], t["beta"], EPS, 2)
+    r = tight.GroupNorm(t["x"], groups, t["gamma"], t["beta"], EPS, 2, run=tight.RUN)
+    within(mean, r.mean, r.e_mean, "mean")
+    within(rstd, r.rstd, r.e_rstd, "rstd")
+    within(y, *r.forward(), "y")
+    check_bwd(mqc, t, groups, 2, tight.RUN)
+
+
+@pytest.mark.parametrize("shape", tight.SLABS)
+def test_drift_over_many_slabs(mqc, shape):
+    *dims, groups = shape
+    t = make(*dims, F32, seed=groups, drift=True)
+    y, mean, rstd = mqc.group_norm_fwd(t["x"], groups, None, None, EPS, 0)
+    r = tight.GroupNorm(t["x"], groups, None, None, EPS, 0, run=tight.RUN)
+    within(mean, r.mean, r.e_mean, "mean")
+    within(rstd, r.rstd, r.e_rstd, "rstd")
+    within(y, *r.forward(), "y")
