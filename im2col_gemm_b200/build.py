@@ -29,13 +29,14 @@ def up_to_date() -> bool:
 
 
 def object_up_to_date(obj: str) -> bool:
-    """Newer than every file of its dependency list (written by nvcc -MD)."""
+    """Newer than every file of its dependency list (written by nvcc -MD; one
+    that was cut short names none, or is not there)."""
     if not os.path.exists(obj) or not os.path.exists(obj + ".d"):
         return False
     with open(obj + ".d") as f:
-        files = f.read().replace("\\\n", " ").split(":", 1)[1].split()
+        files = f.read().replace("\\\n", " ").partition(":")[2].split()
     t = os.path.getmtime(obj)
-    return all(os.path.exists(x) and os.path.getmtime(x) <= t for x in files)
+    return bool(files) and all(os.path.exists(x) and os.path.getmtime(x) <= t for x in files)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -52,15 +53,23 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if not force and object_up_to_date(obj):
             continue
         tmp = obj + f".tmp{os.getpid()}"
-        cmd = [NVCC, *FLAGS, "-MD", "-MF", obj + ".d", "-c", "-o", tmp, unit]
+        cmd = [NVCC, *FLAGS, "-MD", "-MF", tmp + ".d", "-c", "-o", tmp, unit]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         running.append((subprocess.Popen(cmd), cmd, tmp, obj))
-    failed = [cmd for proc, cmd, _, _ in running if proc.wait() != 0]
+    failed = []
+    for proc, cmd, tmp, obj in running:
+        if proc.wait() == 0:
+            # the list first: beside the old object it names what made that old
+            os.replace(tmp + ".d", obj + ".d")
+            os.replace(tmp, obj)
+            continue
+        failed.append(cmd)
+        for left in (tmp, tmp + ".d"):
+            if os.path.exists(left):
+                os.remove(left)
     if failed:
         raise subprocess.CalledProcessError(1, failed[0])
-    for _, _, tmp, obj in running:
-        os.replace(tmp, obj)
     tmp = LIB + f".tmp{os.getpid()}"
     subprocess.check_call([NVCC, *FLAGS, "-shared", "-o", tmp, *objects])
     os.replace(tmp, LIB)
