@@ -173,7 +173,7 @@ struct Silu {
 // becomes 127), are scaled by 2^-63, so that their product stays between 2^-126
 // and 2^128; the last multiplication takes the scale out again and flushes what
 // is below the normal numbers: sigmoid is 0 from z = -88 on, and z sigmoid with
-// it.  128x256x14x14 bf16 backward takes 19.4 us; a branch to reciprocals of
+// it.  128x256x14x14 bf16 backward takes 19.6 us; a branch to reciprocals of
 // their own took 20.2, a bound of 2^62 with 0 for all below 19.7, and that
 // bound alone, 18.8 us, would leave z = -1e20 at -22.
 struct SiluPair {
@@ -190,18 +190,24 @@ struct SiluPair {
     __device__ static __forceinline__ float2 slope(float2 z) { return Silu::slope_of(z, sigmoid(z)); }
 };
 struct Gelu {
+    // P(t), in single operations, whose constants are immediates: pairs would
+    // hold them in registers over a loop that may never take this branch
+    // (128x256x14x14 bf16 backward with SiLU 20.3 us, now 19.6)
+    __device__ static __forceinline__ float tail(float t) {
+        float c = fmaf(-0.0400001481f, t, 0.202324226f);
+        c = fmaf(c, t, -0.376809597f);
+        c = fmaf(c, t, 0.254076332f);
+        c = fmaf(c, t, -0.0142213432f);
+        c = fmaf(c, t, 0.159076944f);
+        c = fmaf(c, t, 0.155645937f);
+        c = fmaf(c, t, 0.15992038f);
+        return fmaf(c, t, -1.27575968e-05f);
+    }
     // Phi(z), with e = exp(-z^2 / 2)
     __device__ static __forceinline__ float2 phi(float2 z, float2 e) {
         const float2 a = make_float2(fabsf(z.x), fabsf(z.y));
         const float2 t = rcp_2(fma2(a, both(0.4f), both(1.f)));
-        float2 c = fma2(both(-0.0400001481f), t, both(0.202324226f));
-        c = fma2(c, t, both(-0.376809597f));
-        c = fma2(c, t, both(0.254076332f));
-        c = fma2(c, t, both(-0.0142213432f));
-        c = fma2(c, t, both(0.159076944f));
-        c = fma2(c, t, both(0.155645937f));
-        c = fma2(c, t, both(0.15992038f));
-        c = mul2(fma2(c, t, both(-1.27575968e-05f)), e);
+        float2 c = mul2(make_float2(tail(t.x), tail(t.y)), e);
         return make_float2(z.x > 0.f ? 1.f - c.x : c.x, z.y > 0.f ? 1.f - c.y : c.y);
     }
     __device__ static __forceinline__ float2 bell(float2 z) {
