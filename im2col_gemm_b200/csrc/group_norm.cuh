@@ -391,9 +391,11 @@ struct GnRing {
 // First pass: mean and squared deviations of each group (or piece) of the slab,
 // about the thread's first value, joined by means and squared deviations (Chan
 // et al.): no large squares are subtracted.  Both forward passes together read
-// 16x64x160x160 bf16 twice and write it once (157 MB) in 32.1 us, 4.9 TB/s;
-// read once it would take 16.3, but no image's group fits an SM, and clusters
-// that share one took 44.
+// 16x64x160x160 bf16 twice and write it once (157 MB) in 32.3 us, 4.9 TB/s;
+// read once it would take 16.3, but a group (four channels, 205 KB) does not
+// quite fit an SM in rows of 8 bytes, and the chunk of 32 channels (1.6 MB, rows
+// of 64 bytes) that the on-chip plan prefers took clusters of 16 and 44 us.
+// (Four groups, 819 KB in rows of 32 bytes, were not timed.)
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_stats_kernel(const __grid_constant__ GnParams P) {
     extern __shared__ __align__(16) uint8_t gn_smem[];
@@ -586,7 +588,7 @@ struct GnSlope {
 // First pass: sums of dz and dz xhat, by channel and (times gamma) by group.
 // dz is computed again by the second pass: both passes read x and g (and SiLU's
 // exponential, twice, keeps the issue slots half busy).  32x128x80x80 fp32:
-// 524 MB in 84 us, 6.2 TB/s; 128x256x14x14 bf16 (64 MB) 19 us.
+// 524 MB in 84 us, 6.2 TB/s; 128x256x14x14 bf16 (64 MB) 19.6 us.
 template <typename T, int VEC, bool UNI>
 __global__ void __launch_bounds__(kPassThreads, 3) gn_bwd_sums_kernel(const __grid_constant__ GnParams P) {
     extern __shared__ __align__(16) uint8_t gn_smem[];

@@ -828,9 +828,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) linear_pair_kernel(const __gr
 // in chunks of 256 steps, a lane 8 of them from 16-byte loads (VEC), and are
 // joined in warp order.  Nothing but the loads' latency stands between the
 // launch and the last byte: 1 x 4096 x 4096 takes 8.5 us, 3.9 TB/s (a plain
-// copy of 6.45 TB/s would read the weights in 5.2); the tensor-core form spends
-// more on filling its pipeline and joining its CTAs (11.4 us).  At 1 x 8192 x
-// 8192, 5.3 TB/s.
+// copy of 6.45 TB/s would read the weights in 5.2; its 1024 blocks find 592
+// places, so that a second, partial round starts with cold loads); the
+// tensor-core form spends more on filling its pipeline and joining its CTAs
+// (11.4 us).  At 1 x 8192 x 8192, 5.3 TB/s.
 template <typename T, int MT, int RN, bool VEC>
 __global__ void __launch_bounds__(256) linear_few_kernel(const LinFew P) {
     __shared__ float sums[8][RN * MT];
@@ -843,7 +844,7 @@ __global__ void __launch_bounds__(256) linear_few_kernel(const LinFew P) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) acc[r][m] = make_float2(0.f, 0.f);
     const int chunks = (P.K + 255) / 256;
-#pragma unroll 1   // 60 registers, four blocks an SM; two steps at once gain nothing
+#pragma unroll 1   // 62 registers, four blocks an SM; two steps at once gain nothing
     for (int c = warp; c < chunks; c += 8) {
         const int k = c * 256 + (VEC ? lane * 8 : lane);
         float wv[RN][8];
