@@ -1,10 +1,16 @@
 """CPU: what an interrupted or failed compilation leaves behind does not pass
 for a finished one."""
+import importlib.util
 import os
 import stat
 
 import pytest
-from im2col_gemm_b200 import build as b
+
+HERE = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+# by its file: the package around it wants the library that it builds
+spec = importlib.util.spec_from_file_location("mqc_build", os.path.join(HERE, "im2col_gemm_b200", "build.py"))
+b = importlib.util.module_from_spec(spec)
+spec.loader.exec_module(b)
 
 
 def test_an_unfinished_dependency_list_is_not_up_to_date(tmp_path):
